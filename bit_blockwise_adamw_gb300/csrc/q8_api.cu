@@ -8,10 +8,15 @@
 #include <string>
 
 #include "q8_internal.h"
+#include "q8_train.h"
 
 namespace {
 
 thread_local std::string g_error;
+
+}  // namespace
+
+namespace q8 {
 
 int fail(int code, const std::string& msg)
 {
@@ -23,6 +28,13 @@ int cuda_fail(cudaError_t err, const char* where)
 {
     return fail(Q8_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(err));
 }
+
+}  // namespace q8
+
+namespace {
+
+using q8::cuda_fail;
+using q8::fail;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -222,6 +234,9 @@ int q8_prepare_device(void)
     if (err == cudaSuccess) err = q8::prepare_step1();
     if (err == cudaSuccess) err = q8::prepare_step16();
     if (err == cudaSuccess) err = q8::prepare_codec();
+    if (err == cudaSuccess) err = q8::prepare_ff();
+    if (err == cudaSuccess) err = q8::prepare_norm();
+    if (err == cudaSuccess) err = q8::prepare_distill();
     if (err != cudaSuccess) return cuda_fail(err, "q8_prepare_device");
     return Q8_OK;
 }

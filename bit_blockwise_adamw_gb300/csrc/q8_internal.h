@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <string>
 #include <cuda_runtime.h>
 
 #include "q8adamw.h"
@@ -161,6 +162,11 @@ static_assert(sizeof(Step8Args) <= 32764, "kernel parameter space");
 static_assert(sizeof(Step1Args) <= 32764, "kernel parameter space");
 static_assert(sizeof(Step16Args) <= 32764, "kernel parameter space");
 static_assert(sizeof(Step32Args) <= 32764, "kernel parameter space");
+
+// The message of the calling host thread's last failure, and the status back
+// (q8_api.cu).
+int fail(int code, const std::string& msg);
+int cuda_fail(cudaError_t err, const char* where);
 
 // Host-side table construction (q8_tables.cu).
 void build_codebook(int kind, float out[256]);
