@@ -1,159 +1,737 @@
 // q8_ff.cu -- the gated feed-forward product (include/q8train.h), forward and
-// backward, as plain tiled fp32 products.
+// backward.
+//
+// Four matrix products carry it, all on one persistent tcgen05 kernel over
+// pairs of CTAs (tile_kernel):
+//   kForward  [g | u] = x [w_gate | w_up]^T       epilogue: h = act(g) u
+//   kGates    the same product again              epilogue: dg, du from dh
+//   kInput    dx = dg w_gate + du w_up            one accumulation over 2 d_ff
+//   kWeight   dw_gate = dg^T x, dw_up = du^T x    two batches
+// A pair owns a 256 x 256 tile of the result: each CTA holds 128 rows of A and
+// half of B's 256 rows, and the pair's tensor cores read both halves, so each
+// operand byte is fetched once for twice the products.  In kForward and kGates
+// the 256 columns are 128 of g beside the same 128 of u (CTA 0 loads w_gate's
+// rows, CTA 1 w_up's), so that one thread of the epilogue finds g and u of its
+// element in its own tensor-memory lane and no intermediate leaves the chip.
+// Operands stay as they lie in memory: an operand whose M or N index is
+// contiguous (weights in kInput, everything in kWeight) is loaded in boxes of
+// 64 of that index by 64 of K and given to the tensor core as MN-major.
+//
+// Roles: warp 0 loads (TMA, a ring of six 32 KB stages in each CTA), warp 1 of
+// the pair's first CTA issues the products, eight warps run the epilogue from
+// tensor memory, whose 512 columns hold two accumulators, so that a tile's
+// epilogue runs under the next tile's products.
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
 #include "q8_internal.h"
+#include "q8_tc.cuh"
 #include "q8_train.h"
 
 namespace q8 {
 
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kPairM = 256, kPairN = 256, kStepK = 64;     // a pair's tile; K to a stage
+constexpr int kHalf = 128;                                 // a CTA's rows of A, and of B
+constexpr int kStages = 6;
+constexpr int kOperandBytes = kHalf * kStepK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kChunkBytes = 64 * kStepK * 2;               // 64 of M or N by 64 of K
+constexpr int kEpilogueWarps = 8;
+constexpr int kTileThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kTileSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kRaster = 8;                                 // row tiles that share a sweep over the columns
 
-// act(g) and act'(g).
-__device__ __forceinline__ float2 activation(float g, int act)
+enum Mode { kForward, kGates, kInput, kWeight };
+
+struct TileArgs {
+    CUtensorMap a[2], b[2];          // kForward, kGates: a[0]; b by CTA.  kInput: by segment.  kWeight: a by batch, b[0]
+    int32_t m_tiles, n_tiles, batches, splits;
+    int32_t k_steps, segments;       // stages of one segment, and segments
+    int64_t M, N;                    // of one batch's result (N = d_ff where two accumulators share a tile)
+    uint16_t* out[2];
+    int64_t out_stride;
+    float* save;                     // kForward: g [M, N], then u, or NULL
+    const uint16_t* dh;              // kGates
+    int64_t dh_stride;
+    float* partial;                  // splits > 1: [batch, split, M, N]
+    int32_t act;
+    int32_t* fault;                  // host-mapped: set when a wait ran out
+};
+
+// act(g) and act'(g).  __expf and __fdividef are within a few units of 2^-23 of
+// their results where these do not vanish.
+__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
+
+__device__ __forceinline__ float act_value(float g, int act)
+{
+    if (act == Q8_SILU) return g * sigmoid(g);
+    if (act == Q8_GELU_TANH)       // (1 + tanh t)/2 = sigmoid(2 t)
+        return g * sigmoid(1.5957691216057308f * g * fmaf(0.044715f, g * g, 1.0f));
+    return 0.5f * g * erfcf(-0.70710678118654752f * g);
+}
+
+__device__ __forceinline__ float2 act_both(float g, int act)
 {
     if (act == Q8_SILU) {
-        const float s = 1.0f / (1.0f + __expf(-g));
+        const float s = sigmoid(g);
         return make_float2(g * s, s * fmaf(g, 1.0f - s, 1.0f));
     }
     if (act == Q8_GELU_TANH) {
-        // 1/2 (1 + tanh(t)) = sigmoid(2 t)
-        constexpr float c = 1.5957691216057308f;              // 2 sqrt(2/pi)
-        const float g2 = g * g;
-        const float s = 1.0f / (1.0f + __expf(-c * g * fmaf(0.044715f, g2, 1.0f)));
-        return make_float2(g * s, s + g * s * (1.0f - s) * c * fmaf(3.0f * 0.044715f, g2, 1.0f));
+        const float g2 = g * g, s = sigmoid(1.5957691216057308f * g * fmaf(0.044715f, g2, 1.0f));
+        return make_float2(g * s, s + g * s * (1.0f - s) * 1.5957691216057308f * fmaf(0.134145f, g2, 1.0f));
     }
     const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
     return make_float2(g * cdf, fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), cdf));
 }
 
-// C[m, n] = sum over the segments s of sum_k A_s(m, k) B_s(n, k), with the
-// operands' strides given: one 64 x 64 tile to a CTA, 4 x 4 to a thread.
-struct Operand {
-    const uint16_t* p[2];
-    int64_t row, col;             // stride of m (or n), and of k
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t r[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+
+// 32 consecutive elements of a row, `left` of which exist: in 32-byte stores
+// where they are whole and aligned, element by element at an edge.
+__device__ __forceinline__ void store_row(uint16_t* p, const float v[32], int64_t left)
+{
+    if (left >= 32 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = pack2(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
+            store32(p + 16 * i, r);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) p[i] = float_to_bf16(v[i]);
+    }
+}
+
+__device__ __forceinline__ void store_row(float* p, const float v[32], int64_t left)
+{
+    if (left >= 32 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store32(p + 8 * i, reinterpret_cast<const uint32_t*>(v + 8 * i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) p[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ void load_row(const uint16_t* p, float v[32], int64_t left)
+{
+    if (left >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i < left ? bf16_to_float(p[i]) : 0.0f;
+    }
+}
+
+// One unit of work: a tile of one batch, over one of `splits` parts of K.
+struct Unit {
+    int batch, split, m, n, k0, k1;
 };
 
-__device__ __forceinline__ void tile_product(const uint16_t* a, int64_t am, int64_t ak, const uint16_t* b, int64_t bn,
-                                             int64_t bk, int64_t m0, int64_t n0, int64_t M, int64_t N, int64_t K,
-                                             float acc[4][4])
+__device__ __forceinline__ Unit unit_of(const TileArgs& a, int i)
 {
-    __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t k0 = 0; k0 < K; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-            const int r = i / kStep, k = i % kStep;
-            sa[k][r] = m0 + r < M && k0 + k < K ? bf16_to_float(a[(m0 + r) * am + (k0 + k) * ak]) : 0.0f;
-            sb[k][r] = n0 + r < N && k0 + k < K ? bf16_to_float(b[(n0 + r) * bn + (k0 + k) * bk]) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
+    Unit u;
+    const int tiles = a.m_tiles * a.n_tiles;
+    const int t = i % tiles;
+    u.split = i / tiles % a.splits;
+    u.batch = i / tiles / a.splits;
+    // kRaster row tiles by all columns at a time, column by column: the tiles
+    // that run at once share rows of both operands, which L2 then holds
+    const int band = t / (kRaster * a.n_tiles), first = band * kRaster;
+    const int rows = min(kRaster, a.m_tiles - first), in = t - first * a.n_tiles;
+    u.m = first + in % rows;
+    u.n = in / rows;
+    const int64_t steps = static_cast<int64_t>(a.k_steps) * a.segments;
+    u.k0 = static_cast<int>(steps * u.split / a.splits);
+    u.k1 = static_cast<int>(steps * (u.split + 1) / a.splits);
+    return u;
 }
 
-// h (and g, u for the backward call), or with dh given dg and du.
-__global__ void __launch_bounds__(256) ff_dual_kernel(const q8_gated_ff f, uint16_t* h, int64_t h_stride, float* saved,
-                                                      const uint16_t* dh, int64_t dh_stride, uint16_t* dg, uint16_t* du)
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
+    tile_kernel(const __grid_constant__ TileArgs args)
 {
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile; m0 < f.tokens; m0 += static_cast<int64_t>(gridDim.y) * kTile) {
-        float g[4][4] = {}, u[4][4] = {};
-        tile_product(f.x, f.x_stride, 1, f.w_gate, f.d_model, 1, m0, n0, f.tokens, f.d_ff, f.d_model, g);
-        tile_product(f.x, f.x_stride, 1, f.w_up, f.d_model, 1, m0, n0, f.tokens, f.d_ff, f.d_model, u);
-        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-                if (m >= f.tokens || n >= f.d_ff) continue;
-                const float2 a = activation(g[i][j], f.act);
-                if (dh) {
-                    const float d = bf16_to_float(dh[m * dh_stride + n]);
-                    dg[m * f.d_ff + n] = float_to_bf16(d * u[i][j] * a.y);
-                    du[m * f.d_ff + n] = float_to_bf16(d * a.x);
-                } else {
-                    h[m * h_stride + n] = float_to_bf16(a.x * u[i][j]);
-                    if (saved) {
-                        saved[m * f.d_ff + n] = g[i][j];
-                        saved[(f.tokens + m) * f.d_ff + n] = u[i][j];
+    constexpr bool kAmn = MODE == kWeight, kBmn = MODE == kInput || MODE == kWeight;
+    constexpr bool kDual = MODE == kForward || MODE == kGates;
+    constexpr uint32_t kDesc = mma_desc(kAmn, kBmn, kPairM, kPairN);
+
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;      // 128-byte swizzle: 1024-byte aligned stages
+    const uint32_t bars = base + kStages * kStageBytes;
+    const auto full = [&](int s) { return bars + 8 * s; };
+    const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+    const auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
+    const auto acc_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
+    const uint32_t done = bars + 8 * (2 * kStages + 4);
+    const uint32_t tmem_slot = done + 8;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int units = args.batches * args.splits * args.m_tiles * args.n_tiles;
+
+    if (warp == 0) {
+        if (elect()) {
+            for (int s = 0; s < kStages; ++s) {
+                bar_init(full(s), 1);
+                bar_init(empty(s), 1);
+            }
+            for (int b = 0; b < 2; ++b) {
+                bar_init(acc_full(b), 1);
+                bar_init(acc_empty(b), 2 * kEpilogueWarps);
+            }
+            bar_init(done, 1);
+            bar_init_fence();
+            tma_prefetch_map(&args.a[0]);
+            tma_prefetch_map(&args.b[0]);
+        }
+    } else if (warp == 1) {
+        tmem_alloc_all(tmem_slot);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+
+    bool ok = true;
+    if (warp == 0) {
+        if (elect()) {
+            int s = 0;
+            uint32_t phase = 1;                       // an empty stage's first wait passes
+            for (int i = pair; i < units && ok; i += pairs) {
+                const Unit u = unit_of(args, i);
+                const int m0 = u.m * kPairM + static_cast<int>(rank) * kHalf;
+                const int n0 = kDual ? u.n * kHalf : u.n * kPairN + static_cast<int>(rank) * kHalf;
+                for (int k = u.k0; k < u.k1; ++k) {
+                    if (!(ok = bar_wait(empty(s), phase))) break;
+                    if (rank == 0) bar_expect(full(s), 2 * kStageBytes);
+                    const uint32_t bar = peer_addr(full(s), 0);
+                    const int seg = MODE == kInput ? k / args.k_steps : 0;
+                    const int x = (MODE == kInput ? k % args.k_steps : k) * kStepK;
+                    const CUtensorMap* a = &args.a[MODE == kWeight ? u.batch : seg];
+                    const CUtensorMap* b = &args.b[kDual ? rank : seg];
+                    const uint32_t sa = base + s * kStageBytes, sb = sa + kOperandBytes;
+                    if (kAmn) {
+                        tma_load(sa, a, m0, x, bar);
+                        tma_load(sa + kChunkBytes, a, m0 + 64, x, bar);
+                    } else {
+                        tma_load(sa, a, x, m0, bar);
                     }
+                    if (kBmn) {
+                        tma_load(sb, b, n0, x, bar);
+                        tma_load(sb + kChunkBytes, b, n0 + 64, x, bar);
+                    } else {
+                        tma_load(sb, b, x, n0, bar);
+                    }
+                    if (++s == kStages) s = 0, phase ^= 1;
                 }
             }
+            // no load may be in flight when the CTA ends: every stage loaded
+            // has been given back (the products over it have completed)
+            for (int i = 0; i < kStages; ++i) {
+                ok = bar_wait(empty(s), phase) && ok;
+                if (++s == kStages) s = 0, phase ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && elect()) {
+            int s = 0, b = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            for (int i = pair; i < units && ok; i += pairs) {
+                const Unit u = unit_of(args, i);
+                if (!(ok = bar_wait(acc_empty(b), acc_phase))) break;
+                tc_fence_after();
+                const uint32_t d = tmem + b * kPairN;
+                for (int k = u.k0; k < u.k1; ++k) {
+                    if (!(ok = bar_wait(full(s), phase))) break;
+                    tc_fence_after();
+                    const uint32_t sa = base + s * kStageBytes, sb = sa + kOperandBytes;
+                    // K-major: 8 rows of 128 bytes to a swizzle atom, K = 16 is 32 bytes on;
+                    // MN-major: 8 of K by 64 of M to an atom, K = 16 is two atoms on
+#pragma unroll
+                    for (int j = 0; j < kStepK / 16; ++j)
+                        mma_pair(d, smem_desc(sa + j * (kAmn ? 2048 : 32), kAmn ? kChunkBytes : 16, 1024),
+                                 smem_desc(sb + j * (kBmn ? 2048 : 32), kBmn ? kChunkBytes : 16, 1024), kDesc,
+                                 k > u.k0 || j > 0);
+                    mma_commit_pair(empty(s));
+                    if (++s == kStages) s = 0, phase ^= 1;
+                }
+                if (!ok) break;
+                mma_commit_pair(acc_full(b));
+                if (++b == 2) b = 0, acc_phase ^= 1;
+            }
+            mma_commit_pair(done);
+            ok = bar_wait(done, 0) && ok;                // tensor memory is freed after this
+        }
+    } else {
+        const int quad = warp & 3, half = (warp - 2) >> 2;       // 32 lanes, and half of the columns
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        int b = 0;
+        uint32_t phase = 0;
+        for (int i = pair; i < units; i += pairs) {
+            const Unit u = unit_of(args, i);
+            const int64_t m = static_cast<int64_t>(u.m) * kPairM + rank * kHalf + quad * 32 + lane;
+            const bool row = m < args.M;
+            if (!(ok = bar_wait(acc_full(b), phase))) break;
+            tc_fence_after();
+            const uint32_t t = lanes + b * kPairN;
+            constexpr int kChunks = kDual ? 2 : 4;
+#pragma unroll 1
+            for (int c = 0; c < kChunks; ++c) {
+                float v[32], w[32];
+                const int col = (half * kChunks + c) * 32;
+                const int64_t n = static_cast<int64_t>(u.n) * (kDual ? kHalf : kPairN) + col;
+                const int64_t left = args.N - n;
+                tmem_load32(t + col, v);
+                if (kDual) tmem_load32(t + kHalf + col, w);
+                tmem_load_wait();
+                if (c == kChunks - 1) {                  // read out: the products may write here again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(peer_addr(acc_empty(b), 0));
+                }
+                if (!row || left <= 0) continue;
+                if (MODE == kForward) {
+                    if (args.save) {
+                        store_row(args.save + m * args.N + n, v, left);
+                        store_row(args.save + (args.M + m) * args.N + n, w, left);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], args.act) * w[j];
+                    store_row(args.out[0] + m * args.out_stride + n, v, left);
+                } else if (MODE == kGates) {
+                    float d[32];
+                    load_row(args.dh + m * args.dh_stride + n, d, left);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float2 a = act_both(v[j], args.act);
+                        v[j] = d[j] * w[j] * a.y;
+                        w[j] = d[j] * a.x;
+                    }
+                    store_row(args.out[0] + m * args.out_stride + n, v, left);
+                    store_row(args.out[1] + m * args.out_stride + n, w, left);
+                } else if (args.splits > 1) {
+                    store_row(args.partial + ((static_cast<int64_t>(u.batch) * args.splits + u.split) * args.M + m) * args.N + n,
+                              v, left);
+                } else {
+                    store_row(args.out[MODE == kWeight ? u.batch : 0] + m * args.out_stride + n, v, left);
+                }
+            }
+            if (++b == 2) b = 0, phase ^= 1;
+        }
+        // the second CTA's copy of the last arrival: it must land before the CTA ends
+        if (rank == 1 && warp == 2) ok = bar_wait(done, 0) && ok;
     }
+    if (!ok) atomicExch_system(args.fault, 1);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) tmem_free_all(tmem);
 }
 
-// dg and du from the saved g and u.
-__global__ void __launch_bounds__(256) ff_gates_kernel(const float* saved, const uint16_t* dh, int64_t dh_stride,
-                                                       int64_t tokens, int64_t d_ff, int act, uint16_t* dg, uint16_t* du)
+// out = the sum of the splits' parts, in their order.
+__global__ void __launch_bounds__(256) join_kernel(const float* partial, int splits, int64_t M, int64_t N, uint16_t* out,
+                                                   int64_t out_stride)
 {
-    const int64_t n = tokens * d_ff;
+    const int64_t n = M * N;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const float2 a = activation(saved[i], act);
-        const float d = bf16_to_float(dh[i / d_ff * dh_stride + i % d_ff]);
-        dg[i] = float_to_bf16(d * saved[n + i] * a.y);
-        du[i] = float_to_bf16(d * a.x);
+        float s = partial[i];
+        for (int k = 1; k < splits; ++k) s += partial[k * n + i];
+        out[i / N * out_stride + i % N] = float_to_bf16(s);
     }
 }
 
-__global__ void __launch_bounds__(256) ff_product_kernel(const Operand a, const Operand b, int segments, int64_t M,
-                                                         int64_t N, int64_t K, uint16_t* c, int64_t c_stride)
+// dg and du from the saved g and u: eight columns of a row to a thread.
+__global__ void __launch_bounds__(256) gates_kernel(const float* save, const uint16_t* dh, int64_t dh_stride, int64_t M,
+                                                    int64_t N, int act, uint16_t* dg, uint16_t* du, int64_t stride)
 {
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile; m0 < M; m0 += static_cast<int64_t>(gridDim.y) * kTile) {
-        float acc[4][4] = {};
-        for (int s = 0; s < segments; ++s)
-            tile_product(a.p[s], a.row, a.col, b.p[s], b.row, b.col, m0, n0, M, N, K, acc);
-        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j)
-                if (m0 + ty * 4 + i < M && n0 + tx * 4 + j < N)
-                    c[(m0 + ty * 4 + i) * c_stride + n0 + tx * 4 + j] = float_to_bf16(acc[i][j]);
+    const int64_t groups = (N + 7) / 8, n = M * groups;
+    const bool whole = (N & 7) == 0 && ((reinterpret_cast<uintptr_t>(save) & 15) == 0) &&
+                       ((reinterpret_cast<uintptr_t>(dh) & 15) == 0) && (dh_stride & 7) == 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t m = i / groups, c = (i - m * groups) * 8;
+        const float *g = save + m * N + c, *u = g + M * N;
+        const uint16_t* d = dh + m * dh_stride + c;
+        float gv[8], uv[8], dv[8];
+        if (whole) {
+            *reinterpret_cast<float4*>(gv) = __ldcs(reinterpret_cast<const float4*>(g));
+            *reinterpret_cast<float4*>(gv + 4) = __ldcs(reinterpret_cast<const float4*>(g) + 1);
+            *reinterpret_cast<float4*>(uv) = __ldcs(reinterpret_cast<const float4*>(u));
+            *reinterpret_cast<float4*>(uv + 4) = __ldcs(reinterpret_cast<const float4*>(u) + 1);
+            const uint4 q = __ldcs(reinterpret_cast<const uint4*>(d));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dv[2 * j] = __uint_as_float(w[j] << 16);
+                dv[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool in = c + j < N;
+                gv[j] = in ? g[j] : 0.0f;
+                uv[j] = in ? u[j] : 0.0f;
+                dv[j] = in ? bf16_to_float(d[j]) : 0.0f;
+            }
+        }
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 f = act_both(gv[j], act);
+            gv[j] = dv[j] * uv[j] * f.y;
+            uv[j] = dv[j] * f.x;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = pack2(gv[2 * j], gv[2 * j + 1]);
+            b[j] = pack2(uv[2 * j], uv[2 * j + 1]);
+        }
+        // the rows' stride is a multiple of 16: the last group's padding is there to be written
+        *reinterpret_cast<uint4*>(dg + m * stride + c) = make_uint4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<uint4*>(du + m * stride + c) = make_uint4(b[0], b[1], b[2], b[3]);
     }
 }
 
-dim3 tiles(int64_t M, int64_t N)
+// A copy whose rows start on 16 bytes, for TMA.
+__global__ void __launch_bounds__(256) align_kernel(const uint16_t* in, int64_t in_stride, int64_t rows, int64_t cols,
+                                                    uint16_t* out, int64_t out_stride)
 {
-    const int64_t y = (M + kTile - 1) / kTile;
-    return dim3(static_cast<unsigned>((N + kTile - 1) / kTile), static_cast<unsigned>(y < 65535 ? y : 65535));
+    const int64_t n = rows * cols;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+        out[i / cols * out_stride + i % cols] = in[i / cols * in_stride + i % cols];
+}
+
+// ------------------------------------------------------------------------- host
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// A bf16 matrix as TMA may read it.
+struct Matrix {
+    const uint16_t* p;
+    int64_t rows, cols, stride;
+};
+
+bool tma_ready(const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; }
+
+// The workspace: aligned copies of x and the weights where TMA cannot read
+// them in place, and for the backward call dg, du and the partial sums.
+struct Layout {
+    int64_t x = -1, w_gate = -1, w_up = -1, dg = -1, du = -1, partial = -1, bytes = 0;
+    int64_t d_stride, f_stride;              // row strides of the copies, and of dg and du
+};
+
+struct Device {
+    int sms = 0;
+    int32_t* fault = nullptr;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+};
+
+// How many parts K is cut into: with fewer tiles than pairs of SMs the idle
+// pairs take parts of K, at least eight stages each (what fills the ring).
+int splits_for(int64_t tiles, int64_t steps, int pairs)
+{
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(pairs / std::max<int64_t>(1, tiles), steps / 8)));
+}
+
+struct Shape {
+    int64_t m_tiles, n_tiles, k_steps;
+    int splits;
+};
+
+Shape input_shape(const q8_gated_ff& f, int pairs)
+{
+    Shape s{ceil_div(f.tokens, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.d_ff, kStepK), 1};
+    s.splits = splits_for(s.m_tiles * s.n_tiles, 2 * s.k_steps, pairs);
+    return s;
+}
+
+Shape weight_shape(const q8_gated_ff& f, int pairs)
+{
+    Shape s{ceil_div(f.d_ff, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.tokens, kStepK), 1};
+    s.splits = splits_for(2 * s.m_tiles * s.n_tiles, s.k_steps, pairs);
+    return s;
+}
+
+std::mutex g_lock;
+std::map<int, Device> g_devices;
+
+cudaError_t device(Device* out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_lock);
+    Device& d = g_devices[dev];
+    if (!d.encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if ((e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found)) != cudaSuccess)
+            return e;
+        if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+        if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        if (!d.fault) {
+            void* p = nullptr;
+            if ((e = cudaHostAlloc(&p, sizeof(int32_t), cudaHostAllocMapped)) != cudaSuccess) return e;
+            d.fault = static_cast<int32_t*>(p);
+            *d.fault = 0;
+        }
+        const void* kernels[] = {
+            reinterpret_cast<const void*>(tile_kernel<kForward>), reinterpret_cast<const void*>(tile_kernel<kGates>),
+            reinterpret_cast<const void*>(tile_kernel<kInput>), reinterpret_cast<const void*>(tile_kernel<kWeight>)};
+        for (const void* k : kernels)
+            if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem)) != cudaSuccess) return e;
+        d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    *out = d;
+    return cudaSuccess;
+}
+
+// A launch that gave up waiting is reported by the next call.
+cudaError_t earlier_fault(const Device& d)
+{
+    volatile int32_t* f = d.fault;
+    if (*f == 0) return cudaSuccess;
+    *f = 0;
+    return cudaErrorLaunchTimeout;
+}
+
+int pairs_of(const Device& d) { return std::max(1, d.sms / 2); }
+
+// Two-dimensional map of m, boxes of box_cols x box_rows with the 128-byte
+// swizzle; what lies outside reads as zeros.
+cudaError_t encode(const Device& d, CUtensorMap* map, const Matrix& m, int box_cols, int box_rows)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m.stride) * 2};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = d.encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(m.p), dims, strides, box,
+                                steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+Layout layout(const q8_gated_ff& f, bool backward, int pairs)
+{
+    Layout l;
+    l.d_stride = round_up(f.d_model, 8);
+    l.f_stride = round_up(f.d_ff, 16);
+    auto take = [&](int64_t bytes) {
+        const int64_t at = l.bytes;
+        l.bytes += round_up(bytes, 256);
+        return at;
+    };
+    if (f.tokens == 0) return l;
+    if (!tma_ready(f.x, f.x_stride)) l.x = take(f.tokens * l.d_stride * 2);
+    if (!tma_ready(f.w_gate, f.d_model)) l.w_gate = take(f.d_ff * l.d_stride * 2);
+    if (!tma_ready(f.w_up, f.d_model)) l.w_up = take(f.d_ff * l.d_stride * 2);
+    if (backward) {
+        l.dg = take(f.tokens * l.f_stride * 2);
+        l.du = take(f.tokens * l.f_stride * 2);
+        const Shape i = input_shape(f, pairs), w = weight_shape(f, pairs);
+        const int64_t need = std::max(i.splits > 1 ? i.splits * f.tokens * f.d_model : 0,
+                                      w.splits > 1 ? 2 * w.splits * f.d_ff * f.d_model : 0);
+        if (need) l.partial = take(need * 4);
+    }
+    return l;
+}
+
+unsigned blocks_for(int64_t n, const Device& d)
+{
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 256), d.sms * int64_t(8))));
+}
+
+// x and the weights as TMA may read them.
+cudaError_t operands(const q8_gated_ff& f, const Layout& l, const Device& d, cudaStream_t st, Matrix m[3])
+{
+    m[0] = Matrix{f.x, f.tokens, f.d_model, f.x_stride};
+    m[1] = Matrix{f.w_gate, f.d_ff, f.d_model, f.d_model};
+    m[2] = Matrix{f.w_up, f.d_ff, f.d_model, f.d_model};
+    const int64_t at[3] = {l.x, l.w_gate, l.w_up};
+    for (int i = 0; i < 3; ++i) {
+        if (at[i] < 0) continue;
+        uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(f.workspace) + at[i]);
+        align_kernel<<<blocks_for(m[i].rows * m[i].cols, d), 256, 0, st>>>(m[i].p, m[i].stride, m[i].rows, m[i].cols, copy,
+                                                                          l.d_stride);
+        m[i].p = copy;
+        m[i].stride = l.d_stride;
+    }
+    return cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t run_tiles(const TileArgs& a, const Device& d, cudaStream_t st)
+{
+    const int64_t units = static_cast<int64_t>(a.batches) * a.splits * a.m_tiles * a.n_tiles;
+    if (units >= (int64_t(1) << 31) - 2 * pairs_of(d)) return cudaErrorInvalidValue;
+    tile_kernel<MODE><<<static_cast<unsigned>(2 * std::min<int64_t>(units, pairs_of(d))), kTileThreads, kTileSmem, st>>>(a);
+    return cudaGetLastError();
+}
+
+// Where the product of x with both weights goes: kForward and kGates.
+cudaError_t dual_args(const q8_gated_ff& f, const Device& d, const Matrix m[3], TileArgs* a)
+{
+    a->m_tiles = static_cast<int32_t>(ceil_div(f.tokens, kPairM));
+    a->n_tiles = static_cast<int32_t>(ceil_div(f.d_ff, kHalf));
+    a->batches = a->splits = a->segments = 1;
+    a->k_steps = static_cast<int32_t>(ceil_div(f.d_model, kStepK));
+    a->M = f.tokens;
+    a->N = f.d_ff;
+    a->act = f.act;
+    a->fault = d.fault;
+    cudaError_t e = encode(d, &a->a[0], m[0], kStepK, kHalf);
+    if (e == cudaSuccess) e = encode(d, &a->b[0], m[1], kStepK, kHalf);
+    if (e == cudaSuccess) e = encode(d, &a->b[1], m[2], kStepK, kHalf);
+    return e;
 }
 
 }  // namespace
 
-cudaError_t prepare_ff() { return cudaSuccess; }
+cudaError_t prepare_ff()
+{
+    Device d;
+    return device(&d);
+}
 
-int64_t ff_workspace(const q8_gated_ff& f, bool backward) { return backward ? 2 * f.tokens * f.d_ff * 2 : 0; }
+int64_t ff_workspace(const q8_gated_ff& f, bool backward)
+{
+    int dev = 0, sms = 0;                                    // sizes do not need a GPU: 152 SMs where there is none
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        sms = 152;
+    }
+    return layout(f, backward, std::max(1, sms / 2)).bytes;
+}
 
 cudaError_t launch_ff_forward(const q8_gated_ff& f, uint16_t* h, int64_t h_stride, float* saved, cudaStream_t st)
 {
-    ff_dual_kernel<<<tiles(f.tokens, f.d_ff), 256, 0, st>>>(f, h, h_stride, saved, nullptr, 0, nullptr, nullptr);
-    return cudaGetLastError();
+    Device d;
+    cudaError_t e = device(&d);
+    if (e == cudaSuccess) e = earlier_fault(d);
+    if (e != cudaSuccess) return e;
+    const Layout l = layout(f, false, pairs_of(d));
+    Matrix m[3];
+    if ((e = operands(f, l, d, st, m)) != cudaSuccess) return e;
+    TileArgs a{};
+    if ((e = dual_args(f, d, m, &a)) != cudaSuccess) return e;
+    a.out[0] = h;
+    a.out_stride = h_stride;
+    a.save = saved;
+    return run_tiles<kForward>(a, d, st);
 }
 
 cudaError_t launch_ff_backward(const q8_gated_ff& f, const FfBackward& b, cudaStream_t st)
 {
-    uint16_t* dg = static_cast<uint16_t*>(f.workspace);
-    uint16_t* du = dg + f.tokens * f.d_ff;
-    if (b.saved)
-        ff_gates_kernel<<<152 * 8, 256, 0, st>>>(b.saved, b.dh, b.dh_stride, f.tokens, f.d_ff, f.act, dg, du);
-    else
-        ff_dual_kernel<<<tiles(f.tokens, f.d_ff), 256, 0, st>>>(f, nullptr, 0, nullptr, b.dh, b.dh_stride, dg, du);
-    if (b.dx)
-        ff_product_kernel<<<tiles(f.tokens, f.d_model), 256, 0, st>>>(
-            Operand{{dg, du}, f.d_ff, 1}, Operand{{f.w_gate, f.w_up}, 1, f.d_model}, 2, f.tokens, f.d_model, f.d_ff,
-            b.dx, b.dx_stride);
-    const uint16_t* d[2] = {dg, du};
-    uint16_t* dw[2] = {b.dw_gate, b.dw_up};
-    for (int i = 0; i < 2; ++i)
-        if (dw[i])
-            ff_product_kernel<<<tiles(f.d_ff, f.d_model), 256, 0, st>>>(
-                Operand{{d[i], nullptr}, 1, f.d_ff}, Operand{{f.x, nullptr}, 1, f.x_stride}, 1, f.d_ff, f.d_model,
-                f.tokens, dw[i], f.d_model);
-    return cudaGetLastError();
+    Device d;
+    cudaError_t e = device(&d);
+    if (e == cudaSuccess) e = earlier_fault(d);
+    if (e != cudaSuccess) return e;
+    const Layout l = layout(f, true, pairs_of(d));
+    uint8_t* ws = static_cast<uint8_t*>(f.workspace);
+    uint16_t *dg = reinterpret_cast<uint16_t*>(ws + l.dg), *du = reinterpret_cast<uint16_t*>(ws + l.du);
+    float* partial = l.partial < 0 ? nullptr : reinterpret_cast<float*>(ws + l.partial);
+    Matrix m[3];
+    if ((e = operands(f, l, d, st, m)) != cudaSuccess) return e;
+    if (b.saved) {
+        gates_kernel<<<blocks_for(f.tokens * ceil_div(f.d_ff, 8), d), 256, 0, st>>>(
+            b.saved, b.dh, b.dh_stride, f.tokens, f.d_ff, f.act, dg, du, l.f_stride);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    } else {
+        TileArgs a{};
+        if ((e = dual_args(f, d, m, &a)) != cudaSuccess) return e;
+        a.out[0] = dg;
+        a.out[1] = du;
+        a.out_stride = l.f_stride;
+        a.dh = b.dh;
+        a.dh_stride = b.dh_stride;
+        if ((e = run_tiles<kGates>(a, d, st)) != cudaSuccess) return e;
+    }
+    const Matrix g{dg, f.tokens, f.d_ff, l.f_stride}, u{du, f.tokens, f.d_ff, l.f_stride};
+    auto join = [&](const TileArgs& a, int batch) {
+        join_kernel<<<blocks_for(a.M * a.N, d), 256, 0, st>>>(a.partial + static_cast<int64_t>(batch) * a.splits * a.M * a.N,
+                                                              a.splits, a.M, a.N, a.out[batch], a.out_stride);
+        return cudaGetLastError();
+    };
+    if (b.dx) {
+        const Shape s = input_shape(f, pairs_of(d));
+        TileArgs a{};
+        a.m_tiles = static_cast<int32_t>(s.m_tiles);
+        a.n_tiles = static_cast<int32_t>(s.n_tiles);
+        a.batches = 1;
+        a.splits = s.splits;
+        a.k_steps = static_cast<int32_t>(s.k_steps);
+        a.segments = 2;
+        a.M = f.tokens;
+        a.N = f.d_model;
+        a.out[0] = b.dx;
+        a.out_stride = b.dx_stride;
+        a.partial = partial;
+        a.fault = d.fault;
+        const Matrix da[2] = {g, u};
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+            e = encode(d, &a.a[i], da[i], kStepK, kHalf);
+            if (e == cudaSuccess) e = encode(d, &a.b[i], m[1 + i], 64, kStepK);
+        }
+        if (e == cudaSuccess) e = run_tiles<kInput>(a, d, st);
+        if (e == cudaSuccess && a.splits > 1) e = join(a, 0);
+        if (e != cudaSuccess) return e;
+    }
+    if (b.dw_gate || b.dw_up) {
+        const Shape s = weight_shape(f, pairs_of(d));
+        TileArgs a{};
+        a.m_tiles = static_cast<int32_t>(s.m_tiles);
+        a.n_tiles = static_cast<int32_t>(s.n_tiles);
+        a.splits = s.splits;
+        a.k_steps = static_cast<int32_t>(s.k_steps);
+        a.segments = 1;
+        a.M = f.d_ff;
+        a.N = f.d_model;
+        a.out_stride = f.d_model;
+        a.partial = partial;
+        a.fault = d.fault;
+        const Matrix da[2] = {g, u};
+        uint16_t* dw[2] = {b.dw_gate, b.dw_up};
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+            if (!dw[i]) continue;
+            a.out[a.batches] = dw[i];
+            e = encode(d, &a.a[a.batches++], da[i], 64, kStepK);
+        }
+        if (e == cudaSuccess) e = encode(d, &a.b[0], m[0], 64, kStepK);
+        if (e == cudaSuccess) e = run_tiles<kWeight>(a, d, st);
+        for (int i = 0; i < a.batches && e == cudaSuccess && a.splits > 1; ++i) e = join(a, i);
+    }
+    return e;
 }
 
 }  // namespace q8
