@@ -302,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             const Unit u = unit_of(args, i);
             const int64_t m = static_cast<int64_t>(u.m) * kPairM + rank * kHalf + quad * 32 + lane;
             const bool row = m < args.M;
-            if (!(ok = bar_wait(acc_full(b), phase))) break;
+            if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(acc_full(b), phase)))) break;
             tc_fence_after();
             const uint32_t t = lanes + b * kPairN;
             constexpr int kChunks = kDual ? 2 : 4;
@@ -451,9 +451,7 @@ struct Layout {
     int64_t d_stride, f_stride;              // row strides of the copies, and of dg and du
 };
 
-struct Device {
-    int sms = 0;
-    int32_t* fault = nullptr;
+struct Device : DeviceInfo {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
@@ -499,13 +497,7 @@ cudaError_t device(Device* out)
         if ((e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found)) != cudaSuccess)
             return e;
         if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-        if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-        if (!d.fault) {
-            void* p = nullptr;
-            if ((e = cudaHostAlloc(&p, sizeof(int32_t), cudaHostAllocMapped)) != cudaSuccess) return e;
-            d.fault = static_cast<int32_t*>(p);
-            *d.fault = 0;
-        }
+        if ((e = device_info(&d)) != cudaSuccess) return e;
         const void* kernels[] = {
             reinterpret_cast<const void*>(tile_kernel<kForward>), reinterpret_cast<const void*>(tile_kernel<kGates>),
             reinterpret_cast<const void*>(tile_kernel<kInput>), reinterpret_cast<const void*>(tile_kernel<kWeight>)};
@@ -515,15 +507,6 @@ cudaError_t device(Device* out)
     }
     *out = d;
     return cudaSuccess;
-}
-
-// A launch that gave up waiting is reported by the next call.
-cudaError_t earlier_fault(const Device& d)
-{
-    volatile int32_t* f = d.fault;
-    if (*f == 0) return cudaSuccess;
-    *f = 0;
-    return cudaErrorLaunchTimeout;
 }
 
 int pairs_of(const Device& d) { return std::max(1, d.sms / 2); }
@@ -638,7 +621,7 @@ cudaError_t launch_ff_forward(const q8_gated_ff& f, uint16_t* h, int64_t h_strid
 {
     Device d;
     cudaError_t e = device(&d);
-    if (e == cudaSuccess) e = earlier_fault(d);
+    if (e == cudaSuccess) e = earlier_fault(d.fault);
     if (e != cudaSuccess) return e;
     const Layout l = layout(f, false, pairs_of(d));
     Matrix m[3];
@@ -655,7 +638,7 @@ cudaError_t launch_ff_backward(const q8_gated_ff& f, const FfBackward& b, cudaSt
 {
     Device d;
     cudaError_t e = device(&d);
-    if (e == cudaSuccess) e = earlier_fault(d);
+    if (e == cudaSuccess) e = earlier_fault(d.fault);
     if (e != cudaSuccess) return e;
     const Layout l = layout(f, true, pairs_of(d));
     uint8_t* ws = static_cast<uint8_t*>(f.workspace);

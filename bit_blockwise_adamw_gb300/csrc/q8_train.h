@@ -16,6 +16,17 @@ cudaError_t prepare_ff();
 cudaError_t prepare_norm();
 cudaError_t prepare_distill();
 
+// The current device's SM count, and the host-mapped word that a kernel sets
+// when one of its waits ran out.
+struct DeviceInfo {
+    int sms = 0;
+    int32_t* fault = nullptr;
+};
+cudaError_t device_info(DeviceInfo* out);
+
+// A launch that gave up waiting is reported by the next call on its device.
+cudaError_t earlier_fault(int32_t* fault);
+
 // Launchers: arguments already checked.
 struct FfBackward {
     const uint16_t* dh;

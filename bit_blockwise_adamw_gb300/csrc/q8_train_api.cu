@@ -2,6 +2,8 @@
 // include/q8train.h: argument checks, then the launchers.
 #include <cmath>
 #include <cstdint>
+#include <map>
+#include <mutex>
 
 #include "q8_internal.h"
 #include "q8_train.h"
@@ -124,7 +126,40 @@ int check_distill(const q8_distill_topk* d)
     return Q8_OK;
 }
 
+std::mutex g_lock;
+std::map<int, q8::DeviceInfo> g_devices;
+
 }  // namespace
+
+namespace q8 {
+
+cudaError_t device_info(DeviceInfo* out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_lock);
+    DeviceInfo& d = g_devices[dev];
+    if (!d.sms && (e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if (!d.fault) {
+        void* p = nullptr;
+        if ((e = cudaHostAlloc(&p, sizeof(int32_t), cudaHostAllocMapped)) != cudaSuccess) return e;
+        d.fault = static_cast<int32_t*>(p);
+        *d.fault = 0;
+    }
+    *out = d;
+    return cudaSuccess;
+}
+
+cudaError_t earlier_fault(int32_t* fault)
+{
+    volatile int32_t* f = fault;
+    if (*f == 0) return cudaSuccess;
+    *f = 0;
+    return cudaErrorLaunchTimeout;
+}
+
+}  // namespace q8
 
 extern "C" {
 
