@@ -269,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             uint32_t phase = 0, acc_phase = 1;
             for (int i = pair; i < units && ok; i += pairs) {
                 const Unit u = unit_of(args, i);
-                if (!(ok = bar_wait(acc_empty(b), acc_phase))) break;
+                if (!(ok = bar_wait<true>(acc_empty(b), acc_phase))) break;
                 tc_fence_after();
                 const uint32_t d = tmem + b * kPairN;
                 for (int k = u.k0; k < u.k1; ++k) {

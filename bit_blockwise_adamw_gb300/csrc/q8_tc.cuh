@@ -70,26 +70,49 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar)
 }
 
 // Wait for the phase of the given parity to complete; false when it has not
-// after about two seconds (2^21 tries that each sleep up to a microsecond).
-// No wait of these kernels lasts as long as a launch, which takes well under a
-// second, so a wait that runs out means the pipeline is broken.
-constexpr uint32_t kWaitTries = 1u << 21;
+// after kWaitTries tries (each polls once, or sleeps for as long as the hardware
+// finds right: a second or more in all).  No wait of these kernels lasts nearly
+// as long, so a wait that runs out means the pipeline is broken.  A time hint on
+// the tries was measured and is left out: sleeping threads then woke up to a
+// microsecond late.
+constexpr uint32_t kWaitTries = 1u << 23;
 
+template <bool CLUSTER>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
 
+// CLUSTER: for a barrier that other CTAs' threads arrive on.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
 {
     for (uint32_t i = 0; i < kWaitTries; ++i)
-        if (bar_try(bar, parity)) return true;
+        if (bar_try<CLUSTER>(bar, parity)) return true;
+    return false;
+}
+
+// The same for a thread that has time: it sleeps between its tries and leaves
+// the issue slots to the others.
+__device__ __forceinline__ bool bar_wait_idle(uint32_t bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < kWaitTries; ++i) {
+        if (bar_try<false>(bar, parity)) return true;
+        __nanosleep(100);
+    }
     return false;
 }
 
@@ -109,6 +132,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// BYTES (4, 8 or 16), aligned to as much, in the thread's current copy group.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map)
