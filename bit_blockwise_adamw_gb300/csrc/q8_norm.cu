@@ -13,10 +13,11 @@
 // nothing is shared in fact; registers would leave room for half the CTAs).
 // A CTA's rows are consecutive, so that a gate's group ends inside a CTA (and
 // is written there) or is one of the two that reach over its ends.  norm_sum
-// and gate_sum add up the CTAs' sums, in their order.
+// adds up the CTAs' sums, in their order.
 #include <algorithm>
 
 #include "q8_internal.h"
+#include "q8_tc.cuh"
 #include "q8_train.h"
 
 namespace q8 {
@@ -42,6 +43,7 @@ struct Backward {
     float* scratch;                  // [cta][wanted sums][dim], where shared memory does not hold them
     int32_t at[kSums];               // index among the wanted sums, -1: not wanted
     int32_t wanted;
+    int32_t* fault;
 };
 
 // ------------------------------------------------------- a thread's columns
@@ -245,7 +247,7 @@ __device__ __forceinline__ float normalise(float (&v)[E], int dim, float inv_dim
 #pragma unroll
     for (int i = 0; i < E; ++i) q[0] = fmaf(v[i], v[i], q[0]);
     red.sum(q);
-    const float rs = 1.0f / sqrtf(fmaf(q[0], inv_dim, eps));
+    const float rs = rsqrtf(fmaf(q[0], inv_dim, eps));
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] *= rs;
     return rs;
@@ -314,34 +316,119 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_forward_kernel
 
 // ------------------------------------------------------------------ backward
 
+constexpr int64_t kMostCtas = 16384;
+
 // Rows [first, stop) of CTA c of `ctas`.
 __host__ __device__ __forceinline__ int64_t first_row(int64_t tokens, int64_t c, int64_t ctas)
 {
-    return tokens / ctas * c + tokens % ctas * c / ctas;
+    const uint32_t n = static_cast<uint32_t>(ctas);          // at most kMostCtas: the product fits
+    return tokens / ctas * c + static_cast<uint32_t>(tokens % ctas) * static_cast<uint32_t>(c) / n;
 }
 
-// Where the thread keeps the sums of its columns: in shared memory, four
-// columns to an access with VEC 8.
-template <int VEC, int E>
-__device__ __forceinline__ void accumulate(float* sums, int dim, const float (&v)[E])
+// The backward kernel works on eight elements (a chunk) at a time, in packed
+// fp32 pairs: what it keeps of a row between its reductions is y, dz and dr' as
+// they came and one fp32 value an element, so that E = 16 fits in 128 registers
+// beside the next row's loads.
+struct Eight {
+    float2 v[4];
+};
+
+template <int E>
+__device__ __forceinline__ Eight chunk_of(const Raw<uint16_t, 8, E>& r, int c)
+{
+    const uint32_t w[4] = {r.q[c].x, r.q[c].y, r.q[c].z, r.q[c].w};
+    Eight e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e.v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+    return e;
+}
+template <int E>
+__device__ __forceinline__ Eight chunk_of(const Raw<float, 8, E>& r, int c)
+{
+    const float4 a = r.q[2 * c], b = r.q[2 * c + 1];
+    return Eight{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+}
+template <typename T, int E>
+__device__ __forceinline__ Eight chunk_of(const Raw<T, 1, E>& r, int c)
+{
+    float v[E];
+    r.get(v);
+    Eight e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e.v[j] = make_float2(v[8 * c + 2 * j], v[8 * c + 2 * j + 1]);
+    return e;
+}
+
+// The column of element j of chunk c.
+template <int VEC>
+__device__ __forceinline__ int column(int c, int j)
+{
+    return VEC == 8 ? (c * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8 + j
+                    : (8 * c + j) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+}
+
+template <int VEC>
+__device__ __forceinline__ Eight channels(const uint16_t* p, int dim, int c)
+{
+    Eight e;
+    if constexpr (VEC == 8) {
+        Raw<uint16_t, 8, 8> r;
+        r.q[0] = column<8>(c, 0) < dim ? __ldg(reinterpret_cast<const uint4*>(p + column<8>(c, 0))) : make_uint4(0, 0, 0, 0);
+        return chunk_of(r, 0);
+    } else {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = column<1>(c, j) < dim ? bf16_to_float(__ldg(p + column<1>(c, j))) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e.v[j] = make_float2(v[2 * j], v[2 * j + 1]);
+        return e;
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void put(uint16_t* row, int dim, int c, const Eight& e)
 {
     if constexpr (VEC == 8) {
-#pragma unroll
-        for (int i = 0; i < E; i += 4)
-            if (inside<8>(i, dim)) {
-                // halves of a chunk apart: consecutive threads on consecutive 16 bytes
-                float4* p = reinterpret_cast<float4*>(sums) + ((i / 4) * blockDim.x + threadIdx.x);
-                float4 s = *p;
-                s.x += v[i];
-                s.y += v[i + 1];
-                s.z += v[i + 2];
-                s.w += v[i + 3];
-                *p = s;
-            }
+        if (column<8>(c, 0) < dim)
+            __stcs(reinterpret_cast<uint4*>(row + column<8>(c, 0)),
+                   make_uint4(pack2(e.v[0].x, e.v[0].y), pack2(e.v[1].x, e.v[1].y), pack2(e.v[2].x, e.v[2].y),
+                              pack2(e.v[3].x, e.v[3].y)));
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (inside<1>(i, dim)) sums[i * blockDim.x + threadIdx.x] += v[i];
+        for (int j = 0; j < 8; ++j)
+            if (column<1>(c, j) < dim) row[column<1>(c, j)] = float_to_bf16(j & 1 ? e.v[j / 2].y : e.v[j / 2].x);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void put(float* row, int dim, int c, const Eight& e)
+{
+    if constexpr (VEC == 8) {
+        if (column<8>(c, 0) < dim) {
+            float4* p = reinterpret_cast<float4*>(row + column<8>(c, 0));
+            __stcs(p, make_float4(e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y));
+            __stcs(p + 1, make_float4(e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (column<1>(c, j) < dim) row[column<1>(c, j)] = j & 1 ? e.v[j / 2].y : e.v[j / 2].x;
+    }
+}
+
+// Sums of a chunk's columns: two 16-byte halves, each of consecutive threads on
+// consecutive addresses; the columns' order among them is the threads' own.
+__device__ __forceinline__ float4* sums_at(float* sums, int c, int half)
+{
+    return reinterpret_cast<float4*>(sums) + (2 * c + half) * blockDim.x + threadIdx.x;
+}
+__device__ __forceinline__ void accumulate(float* sums, int c, const Eight& e)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float4* p = sums_at(sums, c, h);
+        const float4 s = *p;
+        const float2 a = __fadd2_rn(make_float2(s.x, s.y), e.v[2 * h]), b = __fadd2_rn(make_float2(s.z, s.w), e.v[2 * h + 1]);
+        *p = make_float4(a.x, a.y, b.x, b.y);
     }
 }
 
@@ -349,40 +436,112 @@ __device__ __forceinline__ void accumulate(float* sums, int dim, const float (&v
 template <int VEC, int E, typename Out>
 __device__ __forceinline__ void flush(float* sums, int dim, Out* row)
 {
-    float v[E];
-    if constexpr (VEC == 8) {
 #pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            float4* p = reinterpret_cast<float4*>(sums) + ((i / 4) * blockDim.x + threadIdx.x);
-            const float4 s = *p;
-            v[i] = s.x;
-            v[i + 1] = s.y;
-            v[i + 2] = s.z;
-            v[i + 3] = s.w;
-            *p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-    } else {
+    for (int c = 0; c < E / 8; ++c) {
+        const float4 a = *sums_at(sums, c, 0), b = *sums_at(sums, c, 1);
+        *sums_at(sums, c, 0) = *sums_at(sums, c, 1) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const Eight e{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+        if (VEC == 8 && (reinterpret_cast<uintptr_t>(row) & 15) != 0) {       // a gate's gradient may lie on any address
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            v[i] = sums[i * blockDim.x + threadIdx.x];
-            sums[i * blockDim.x + threadIdx.x] = 0.0f;
+            for (int j = 0; j < 8; ++j)
+                if (column<VEC>(c, j) < dim) {
+                    const float v = j & 1 ? e.v[j / 2].y : e.v[j / 2].x;
+                    if constexpr (sizeof(Out) == 2) row[column<VEC>(c, j)] = float_to_bf16(v);
+                    else row[column<VEC>(c, j)] = v;
+                }
+        } else {
+            put<VEC>(row, dim, c, e);
         }
     }
-    if constexpr (sizeof(Out) == 2 && VEC == 8) {
-        // a gate's gradient may lie on any address
-        if ((reinterpret_cast<uintptr_t>(row) & 15) != 0) {
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (inside<8>(i, dim)) row[((i / 8) * blockDim.x + threadIdx.x) * 8 + (i & 7)] = float_to_bf16(v[i]);
-            return;
-        }
-    }
-    put<VEC>(row, dim, v);
 }
 
-template <typename R, int VEC, int E, int MAXT, int CTAS>
-__global__ void __launch_bounds__(MAXT, CTAS) norm_backward_kernel(const __grid_constant__ Backward a)
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Eight operator*(const Eight& a, const Eight& b)
 {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = __fmul2_rn(a.v[j], b.v[j]);
+    return r;
+}
+__device__ __forceinline__ Eight operator*(const Eight& a, float b)
+{
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = __fmul2_rn(a.v[j], both(b));
+    return r;
+}
+__device__ __forceinline__ Eight operator+(const Eight& a, const Eight& b)
+{
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = __fadd2_rn(a.v[j], b.v[j]);
+    return r;
+}
+__device__ __forceinline__ Eight operator+(const Eight& a, float b)
+{
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = __fadd2_rn(a.v[j], both(b));
+    return r;
+}
+// a b + c
+__device__ __forceinline__ Eight fma8(const Eight& a, const Eight& b, const Eight& c)
+{
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = __ffma2_rn(a.v[j], b.v[j], c.v[j]);
+    return r;
+}
+__device__ __forceinline__ Eight fma8(const Eight& a, float b, const Eight& c)
+{
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = __ffma2_rn(a.v[j], both(b), c.v[j]);
+    return r;
+}
+__device__ __forceinline__ void add_dot(float2& s, const Eight& a, const Eight& b)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = __ffma2_rn(a.v[j], b.v[j], s);
+}
+__device__ __forceinline__ void add_all(float2& s, const Eight& a)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = __fadd2_rn(s, a.v[j]);
+}
+// Elements past the row's end become 0.
+template <int VEC>
+__device__ __forceinline__ Eight masked(const Eight& a, int c, int dim)
+{
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        r.v[j] = make_float2(column<VEC>(c, 2 * j) < dim ? a.v[j].x : 0.0f, column<VEC>(c, 2 * j + 1) < dim ? a.v[j].y : 0.0f);
+    return r;
+}
+
+// A vector of all channels as it lies in memory; ones where there is none.
+template <int VEC, int E>
+__device__ __forceinline__ void hold(Raw<uint16_t, VEC, E>& r, const uint16_t* p, int dim)
+{
+    if (p) {
+        r.load(p, dim);
+    } else if constexpr (VEC == 8) {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) r.q[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) r.q[i] = 0x3F80;
+    }
+}
+
+// LAYER: one of the two norms is a layer norm (its means cost reductions that
+// other launches do without).  The weights and the gate's row stay in registers:
+// read again for each row, their latencies were what a row took longest for.
+template <typename R, int VEC, int E, int MAXT, bool LAYER>
+__global__ void __launch_bounds__(MAXT, 1) norm_backward_kernel(const __grid_constant__ Backward a)
+{
+    constexpr int C = E / 8;
     extern __shared__ float4 s_sums4[];
     __shared__ float s_part[128];
     Reducer red{s_part};
@@ -400,7 +559,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_backward_kernel(const __grid_
     R* dr = static_cast<R*>(g.d_residual);
     const int64_t first = first_row(n.tokens, blockIdx.x, gridDim.x), stop = first_row(n.tokens, blockIdx.x + 1, gridDim.x);
     int64_t group = n.gate ? first / n.gate_tokens : 0;
-    int64_t group_end = n.gate ? (group + 1) * n.gate_tokens : n.tokens;      // tokens * 2 at most: no overflow
+    int64_t group_end = n.gate ? (group + 1) * n.gate_tokens : n.tokens;
     const int64_t first_group = group;
 
     // the group's gate gradient: to its place where the CTA has all of the group,
@@ -412,9 +571,14 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_backward_kernel(const __grid_
         else
             flush<VEC, E>(sum_of(kGate), dim, a.gate_partial + (2 * static_cast<int64_t>(blockIdx.x) + (group != first_group)) * n.dim);
     };
+    const auto reduce = [&](float2 s) {
+        float t[1] = {s.x + s.y};
+        red.sum(t);
+        return t[0];
+    };
 
-    Raw<uint16_t, VEC, E> y_next, dz_next;
-    Raw<R, VEC, E> r_next, dr_next;
+    Raw<uint16_t, VEC, E> y_next, dz_next{};
+    Raw<R, VEC, E> r_next, dr_next{};
     const auto load = [&](int64_t t) {
         y_next.load(n.y + t * n.y_stride, dim);
         r_next.load(residual + t * n.residual_stride, dim);
@@ -422,107 +586,121 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_backward_kernel(const __grid_
         if (dr_out) dr_next.load(dr_out + t * g.d_residual_out_stride, dim);
     };
     load(first);
+    Raw<uint16_t, VEC, E> w, gate, pw;
+    hold(w, n.post_weight, dim);
+    hold(pw, n.pre_weight, dim);
+    hold(gate, n.gate ? n.gate + group * n.dim : nullptr, dim);
     for (int64_t t = first; t < stop; ++t) {
         if (t == group_end) {
             flush_gate(t);
             ++group;
             group_end += n.gate_tokens;
+            hold(gate, n.gate + group * n.dim, dim);
         }
-        float yn[E], rn[E], dz[E], d[E], w[E], gate[E];
-        y_next.get(yn);
-        r_next.get(rn);
-#pragma unroll
-        for (int i = 0; i < E; ++i) dz[i] = d[i] = 0.0f;
-        if (g.dz) dz_next.get(dz);
-        if (dr_out) dr_next.get(d);
+        const Raw<uint16_t, VEC, E> y = y_next, dz = dz_next;
+        const Raw<R, VEC, E> r = r_next, dro = dr_next;
         if (t + 1 < stop) load(t + 1);
-
-        // both norms again
-        const float y_rs = normalise<VEC>(yn, dim, inv_dim, n.post_kind, n.eps, red);
-        channels<VEC>(n.gate ? n.gate + group * n.dim : nullptr, dim, 1.0f, gate);
-        channels<VEC>(n.post_weight, dim, 1.0f, w);
-        if (n.post_bias) {
-            float bias[E];
-            channels<VEC>(n.post_bias, dim, 0.0f, bias);
-#pragma unroll
-            for (int i = 0; i < E; ++i) rn[i] = fmaf(n.residual_scale, rn[i], gate[i] * fmaf(yn[i], w[i], bias[i]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) rn[i] = fmaf(n.residual_scale, rn[i], gate[i] * (yn[i] * w[i]));
-        }
-        const float r_rs = normalise<VEC>(rn, dim, inv_dim, n.pre_kind, n.eps, red);
-
-        // d: the gradient of r'
-        if (g.dz) {
-            if (a.at[kPreBias] >= 0) accumulate<VEC>(sum_of(kPreBias), dim, dz);
-            if (a.at[kPreWeight] >= 0) {
-                float p[E];
-#pragma unroll
-                for (int i = 0; i < E; ++i) p[i] = dz[i] * rn[i];
-                accumulate<VEC>(sum_of(kPreWeight), dim, p);
-            }
-            if (n.pre_weight) {
-                float pw[E];
-                channels<VEC>(n.pre_weight, dim, 1.0f, pw);
-#pragma unroll
-                for (int i = 0; i < E; ++i) dz[i] *= pw[i];
-            }
-            if (n.pre_kind != Q8_NORM_NONE) {
-                float s[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    s[0] = fmaf(dz[i], rn[i], s[0]);
-                    s[1] += dz[i];
-                }
-                red.sum(s);
-                const float dot = s[0] * inv_dim, mean = n.pre_kind == Q8_NORM_LAYER ? s[1] * inv_dim : 0.0f;
-#pragma unroll
-                for (int i = 0; i < E; ++i) d[i] = fmaf(r_rs, fmaf(-rn[i], dot, dz[i] - mean), d[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) d[i] += dz[i];
-            }
-        }
-        if (dr) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) dz[i] = n.residual_scale * d[i];
-            put<VEC>(dr + t * g.d_residual_stride, dim, dz);
-        }
-        if (a.at[kGate] >= 0) {
-            if (n.post_bias) {
-                channels<VEC>(n.post_bias, dim, 0.0f, dz);
-#pragma unroll
-                for (int i = 0; i < E; ++i) dz[i] = d[i] * fmaf(yn[i], w[i], dz[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) dz[i] = d[i] * (yn[i] * w[i]);
-            }
-            accumulate<VEC>(sum_of(kGate), dim, dz);
-        }
-        // d: the gradient of N_post(y), then of the normalised y
-#pragma unroll
-        for (int i = 0; i < E; ++i) d[i] *= gate[i];
-        if (a.at[kPostBias] >= 0) accumulate<VEC>(sum_of(kPostBias), dim, d);
-        if (a.at[kPostWeight] >= 0) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) dz[i] = d[i] * yn[i];
-            accumulate<VEC>(sum_of(kPostWeight), dim, dz);
-        }
-        if (!g.d_y) continue;
+        // y's statistics
+        float y_rs = 1.0f, y_mean = 0.0f;
+        const bool y_layer = LAYER && n.post_kind == Q8_NORM_LAYER, r_layer = LAYER && n.pre_kind == Q8_NORM_LAYER;
         if (n.post_kind != Q8_NORM_NONE) {
-            float s[2] = {0.0f, 0.0f};
+            if (y_layer) {
+                float2 s = both(0.0f);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                d[i] *= w[i];
-                s[0] = fmaf(d[i], yn[i], s[0]);
-                s[1] += inside<VEC>(i, dim) ? d[i] : 0.0f;
+                for (int c = 0; c < C; ++c) add_all(s, chunk_of(y, c));
+                y_mean = reduce(s) * inv_dim;
             }
-            red.sum(s);
-            const float dot = s[0] * inv_dim, mean = n.post_kind == Q8_NORM_LAYER ? s[1] * inv_dim : 0.0f;
+            float2 s = both(0.0f);
 #pragma unroll
-            for (int i = 0; i < E; ++i) d[i] = y_rs * fmaf(-yn[i], dot, d[i] - mean);
+            for (int c = 0; c < C; ++c) {
+                Eight e = chunk_of(y, c);
+                if (y_layer) e = masked<VEC>(e + -y_mean, c, dim);
+                add_dot(s, e, e);
+            }
+            y_rs = rsqrtf(fmaf(reduce(s), inv_dim, n.eps));
         }
-        put<VEC>(g.d_y + t * g.d_y_stride, dim, d);
+        const auto yn_of = [&](int c) {
+            const Eight e = chunk_of(y, c);
+            return (y_layer ? e + -y_mean : e) * y_rs;
+        };
+        // r', then normalised
+        Eight rn[C];
+        {
+            float2 s = both(0.0f);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                Eight p = yn_of(c) * chunk_of(w, c);
+                if (n.post_bias) p = p + channels<VEC>(n.post_bias, dim, c);
+                rn[c] = fma8(chunk_of(r, c), n.residual_scale, p * chunk_of(gate, c));
+                if (LAYER) rn[c] = masked<VEC>(rn[c], c, dim);
+                if (r_layer) add_all(s, rn[c]);
+                else add_dot(s, rn[c], rn[c]);
+            }
+            if (r_layer) {
+                const float mean = reduce(s) * inv_dim;
+                s = both(0.0f);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    rn[c] = masked<VEC>(rn[c] + -mean, c, dim);
+                    add_dot(s, rn[c], rn[c]);
+                }
+            }
+            if (n.pre_kind != Q8_NORM_NONE) s.x = reduce(s);
+            const float rs = n.pre_kind == Q8_NORM_NONE ? 1.0f : rsqrtf(fmaf(s.x, inv_dim, n.eps));
+#pragma unroll
+            for (int c = 0; c < C; ++c) rn[c] = rn[c] * rs;
+            // d, the gradient of r', comes from dz through the norm
+            float dot = 0.0f, mean = 0.0f;
+            if (g.dz) {
+                float2 sd = both(0.0f), sm = both(0.0f);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    Eight e = chunk_of(dz, c);
+                    if (a.at[kPreBias] >= 0) accumulate(sum_of(kPreBias), c, e);
+                    if (a.at[kPreWeight] >= 0) accumulate(sum_of(kPreWeight), c, e * rn[c]);
+                    e = e * chunk_of(pw, c);
+                    add_dot(sd, e, rn[c]);
+                    if (r_layer) add_all(sm, e);
+                }
+                if (n.pre_kind != Q8_NORM_NONE) dot = reduce(sd) * inv_dim;
+                if (r_layer) mean = reduce(sm) * inv_dim;
+            }
+            // d, dr, and the gradient of the normalised y (kept in rn)
+            float2 sd = both(0.0f), sm = both(0.0f);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                Eight d = chunk_of(dro, c);
+                if (g.dz) {
+                    Eight e = chunk_of(dz, c) * chunk_of(pw, c);
+                    e = fma8(rn[c], -dot, r_layer ? e + -mean : e);
+                    d = fma8(e, rs, d);
+                }
+                if (dr) put<VEC>(dr + t * g.d_residual_stride, dim, c, d * n.residual_scale);
+                const Eight yn = yn_of(c);
+                const Eight dw = d * chunk_of(w, c), gc = chunk_of(gate, c);
+                if (a.at[kGate] >= 0) {
+                    Eight p = dw * yn;
+                    if (n.post_bias) p = fma8(d, channels<VEC>(n.post_bias, dim, c), p);
+                    accumulate(sum_of(kGate), c, p);
+                }
+                if (a.at[kPostBias] >= 0) accumulate(sum_of(kPostBias), c, d * gc);
+                if (a.at[kPostWeight] >= 0) accumulate(sum_of(kPostWeight), c, d * gc * yn);
+                d = dw * gc;
+                if (LAYER) d = masked<VEC>(d, c, dim);
+                add_dot(sd, d, yn);
+                if (y_layer) add_all(sm, d);
+                rn[c] = d;
+            }
+            if (!g.d_y) continue;
+            dot = mean = 0.0f;
+            if (n.post_kind != Q8_NORM_NONE) dot = reduce(sd) * inv_dim;
+            if (y_layer) mean = reduce(sm) * inv_dim;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Eight e = fma8(yn_of(c), -dot, y_layer ? rn[c] + -mean : rn[c]);
+                put<VEC>(g.d_y + t * g.d_y_stride, dim, c, e * y_rs);
+            }
+        }
     }
     if (first < stop) flush_gate(stop);
     for (int which = 0; which < kGate; ++which)
@@ -530,17 +708,248 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_backward_kernel(const __grid_
             flush<VEC, E>(sum_of(which), dim, a.partial + (static_cast<int64_t>(a.at[which]) * gridDim.x + blockIdx.x) * n.dim);
 }
 
-// Columns of the CTAs' sums: 32 columns to a block, its 16 warps take every
-// 16th row, and their sums are added in order.
+// The same with the rows staged: one thread copies the four rows of the next
+// token to shared memory (bulk copies) while this one's are worked on, so that a
+// thread holds eight columns in 64 registers and an SM 32 warps; with the rows
+// in registers 16 warps wait for one another's reductions half of the time
+// (16384 x 4096 with three sums: 303 us with the rows in registers, 226 us
+// staged).  Rows on 16 bytes.
+template <typename R, bool LAYER, int MAXT, int CTAS>
+__global__ void __launch_bounds__(MAXT, CTAS) norm_staged_kernel(const __grid_constant__ Backward a)
+{
+    extern __shared__ float4 s_sums4[];
+    __shared__ float s_part[128];
+    __shared__ __align__(8) uint64_t s_full[2];
+    Reducer red{s_part};
+    const q8_block_norm& n = a.n;
+    const q8_block_norm_grads& g = a.g;
+    const int dim = static_cast<int>(n.dim), span = 8 * blockDim.x, tid = threadIdx.x;
+    const float inv_dim = 1.0f / dim;
+    const bool mine = tid * 8 < dim;
+    float* sums = reinterpret_cast<float*>(s_sums4);
+    for (int i = tid; i < a.wanted * span; i += blockDim.x) sums[i] = 0.0f;
+    const auto sum_of = [&](int which) { return sums + a.at[which] * span; };
+    // a stage: y, dz, r, dr'
+    uint8_t* stages = reinterpret_cast<uint8_t*>(sums + a.wanted * span);
+    const int half = dim * 2, wide = dim * static_cast<int>(sizeof(R)), stage_bytes = 2 * half + 2 * wide;
+
+    const int64_t first = first_row(n.tokens, blockIdx.x, gridDim.x), stop = first_row(n.tokens, blockIdx.x + 1, gridDim.x);
+    int64_t group = n.gate ? first / n.gate_tokens : 0;
+    int64_t group_end = n.gate ? (group + 1) * n.gate_tokens : n.tokens;
+    const int64_t first_group = group;
+    const auto flush_gate = [&](int64_t end) {
+        if (a.at[kGate] < 0) return;
+        if (group * n.gate_tokens >= first && (end == group_end || end == n.tokens))
+            flush<8, 8>(sum_of(kGate), dim, g.d_gate + group * n.dim);
+        else
+            flush<8, 8>(sum_of(kGate), dim, a.gate_partial + (2 * static_cast<int64_t>(blockIdx.x) + (group != first_group)) * n.dim);
+    };
+    const auto reduce = [&](float2 s) {
+        float t[1] = {s.x + s.y};
+        red.sum(t);
+        return t[0];
+    };
+    const auto fetch = [&](int64_t t, int stage) {
+        const uint32_t bar = smem_addr(&s_full[stage]), to = smem_addr(stages + stage * stage_bytes);
+        bar_expect(bar, half + wide + (g.dz ? half : 0) + (g.d_residual_out ? wide : 0));
+        bulk_load(to, n.y + t * n.y_stride, half, bar);
+        if (g.dz) bulk_load(to + half, g.dz + t * g.dz_stride, half, bar);
+        bulk_load(to + 2 * half, static_cast<const R*>(n.residual) + t * n.residual_stride, wide, bar);
+        if (g.d_residual_out)
+            bulk_load(to + 2 * half + wide, static_cast<const R*>(g.d_residual_out) + t * g.d_residual_out_stride, wide, bar);
+    };
+    if (tid == 0) {
+        bar_init(smem_addr(&s_full[0]), 1);
+        bar_init(smem_addr(&s_full[1]), 1);
+        bar_init_fence();
+    }
+    __syncthreads();
+    if (tid == 0) fetch(first, 0);
+
+    Raw<uint16_t, 8, 8> w, gate, pw;
+    hold(w, n.post_weight, dim);
+    hold(pw, n.pre_weight, dim);
+    hold(gate, n.gate ? n.gate + group * n.dim : nullptr, dim);
+    R* dr = static_cast<R*>(g.d_residual);
+    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t t = first; t < stop; ++t) {
+        if (t == group_end) {
+            flush_gate(t);
+            ++group;
+            group_end += n.gate_tokens;
+            hold(gate, n.gate + group * n.dim, dim);
+        }
+        const uint8_t* at = stages + stage * stage_bytes;
+        const auto eight = [&](const uint8_t* p) {
+            Raw<uint16_t, 8, 8> r;
+            r.q[0] = mine ? reinterpret_cast<const uint4*>(p)[tid] : make_uint4(0, 0, 0, 0);
+            return chunk_of(r, 0);
+        };
+        const auto eight_r = [&](const uint8_t* p) {
+            Raw<R, 8, 8> r;
+            if constexpr (sizeof(R) == 2) {
+                return eight(p);
+            } else {
+                r.q[0] = mine ? reinterpret_cast<const float4*>(p)[2 * tid] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                r.q[1] = mine ? reinterpret_cast<const float4*>(p)[2 * tid + 1] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                return chunk_of(r, 0);
+            }
+        };
+        if (ok) ok = bar_wait(smem_addr(&s_full[stage]), phase);
+
+        // y's statistics
+        const bool y_layer = LAYER && n.post_kind == Q8_NORM_LAYER, r_layer = LAYER && n.pre_kind == Q8_NORM_LAYER;
+        float y_rs = 1.0f, y_mean = 0.0f;
+        if (y_layer) {
+            float2 s = both(0.0f);
+            add_all(s, eight(at));
+            y_mean = reduce(s) * inv_dim;
+        }
+        float2 s = both(0.0f);
+        {
+            Eight e = eight(at);
+            if (y_layer) e = masked<8>(e + -y_mean, 0, dim);
+            add_dot(s, e, e);
+        }
+        const float y_sq = reduce(s);                // all have left the row before: its stage is free
+        if (n.post_kind != Q8_NORM_NONE) y_rs = rsqrtf(fmaf(y_sq, inv_dim, n.eps));
+        if (tid == 0 && t + 1 < stop) fetch(t + 1, stage ^ 1);
+        const auto yn_of = [&]() {
+            const Eight e = eight(at);
+            return (y_layer ? e + -y_mean : e) * y_rs;
+        };
+
+        // r', then normalised
+        Eight rn;
+        {
+            Eight p = yn_of() * chunk_of(w, 0);
+            if (n.post_bias) p = p + channels<8>(n.post_bias, dim, 0);
+            rn = fma8(eight_r(at + 2 * half), n.residual_scale, p * chunk_of(gate, 0));
+        }
+        float rs = 1.0f;
+        if (n.pre_kind != Q8_NORM_NONE) {
+            if (r_layer) {
+                s = both(0.0f);
+                rn = masked<8>(rn, 0, dim);
+                add_all(s, rn);
+                rn = masked<8>(rn + -(reduce(s) * inv_dim), 0, dim);
+            }
+            s = both(0.0f);
+            add_dot(s, rn, rn);
+            rs = rsqrtf(fmaf(reduce(s), inv_dim, n.eps));
+            rn = rn * rs;
+        }
+
+        // d, the gradient of r': from dz through the norm, and from dr'
+        Eight d = g.d_residual_out ? eight_r(at + 2 * half + wide) : Eight{};
+        if (g.dz) {
+            Eight e = eight(at + half);
+            if (a.at[kPreBias] >= 0) accumulate(sum_of(kPreBias), 0, e);
+            if (a.at[kPreWeight] >= 0) accumulate(sum_of(kPreWeight), 0, e * rn);
+            e = e * chunk_of(pw, 0);
+            if (n.pre_kind != Q8_NORM_NONE) {
+                s = both(0.0f);
+                add_dot(s, e, rn);
+                const float dot = reduce(s) * inv_dim;
+                if (r_layer) {
+                    s = both(0.0f);
+                    add_all(s, e);
+                    e = e + -(reduce(s) * inv_dim);
+                }
+                e = fma8(rn, -dot, e);
+            }
+            d = fma8(e, rs, d);
+        }
+        if (dr) put<8>(dr + t * g.d_residual_stride, dim, 0, d * n.residual_scale);
+        const Eight yn = yn_of(), gc = chunk_of(gate, 0);
+        const Eight dw = d * chunk_of(w, 0);
+        if (a.at[kGate] >= 0) {
+            Eight p = dw * yn;
+            if (n.post_bias) p = fma8(d, channels<8>(n.post_bias, dim, 0), p);
+            accumulate(sum_of(kGate), 0, p);
+        }
+        if (a.at[kPostBias] >= 0) accumulate(sum_of(kPostBias), 0, d * gc);
+        if (a.at[kPostWeight] >= 0) accumulate(sum_of(kPostWeight), 0, d * gc * yn);
+        d = dw * gc;
+        if (g.d_y) {
+            if (n.post_kind != Q8_NORM_NONE) {
+                if (LAYER) d = masked<8>(d, 0, dim);
+                s = both(0.0f);
+                add_dot(s, d, yn);
+                const float dot = reduce(s) * inv_dim;
+                if (y_layer) {
+                    s = both(0.0f);
+                    add_all(s, d);
+                    d = d + -(reduce(s) * inv_dim);
+                }
+                d = fma8(yn, -dot, d) * y_rs;
+            }
+            put<8>(g.d_y + t * g.d_y_stride, dim, 0, d);
+        }
+        if ((stage ^= 1) == 0) phase ^= 1;
+    }
+    if (!ok) {                                       // leave no copy in flight
+        atomicExch_system(a.fault, 1);
+        bar_wait(smem_addr(&s_full[stage]), phase);
+        bar_wait(smem_addr(&s_full[stage ^ 1]), phase ^ stage ^ 1);
+    }
+    if (first < stop) flush_gate(stop);
+    for (int which = 0; which < kGate; ++which)
+        if (a.at[which] >= 0)
+            flush<8, 8>(sum_of(which), dim, a.partial + (static_cast<int64_t>(a.at[which]) * gridDim.x + blockIdx.x) * n.dim);
+}
+
+// What the CTAs have of each sum, added up: 32 columns to a block, its 16 warps
+// take every 16th CTA, and their sums are added in order.  blockIdx.y: the
+// weights' sums, then the gate's groups (or, where these are more than the CTAs,
+// the CTAs' ends: only a group that more than one CTA has rows of is summed
+// here).
 struct SumArgs {
-    const float* partial;
-    uint16_t* out[kGate];
-    int64_t rows, dim;
+    const float *partial, *gate_partial;
+    uint16_t *out[kGate], *gate_out;
+    int64_t ctas, dim, tokens, gate_tokens;
+    int32_t count;                   // of the weights' sums
 };
 
-__device__ __forceinline__ void sum_columns(float s, int64_t col, int64_t dim, uint16_t* out)
+__global__ void __launch_bounds__(512) norm_sum_kernel(const __grid_constant__ SumArgs a)
 {
     __shared__ float part[16][33];
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x, dim = a.dim;
+    uint16_t* out;
+    float s = 0.0f;
+    if (static_cast<int>(blockIdx.y) < a.count) {
+        const float* p = a.partial + blockIdx.y * a.ctas * dim + col;
+        if (col < dim) {
+#pragma unroll 8
+            for (int64_t c = threadIdx.y; c < a.ctas; c += 16) s += p[c * dim];
+        }
+        out = a.out[blockIdx.y];
+    } else {
+        const int64_t y = blockIdx.y - a.count, groups = (a.tokens + a.gate_tokens - 1) / a.gate_tokens;
+        const auto first = [&](int64_t c) { return first_row(a.tokens, c, a.ctas); };
+        int64_t begin, cta;                          // the group's first row, and the CTA that has it
+        if (groups < a.ctas) {
+            begin = y * a.gate_tokens;               // below 2^40, the CTAs at most 2^14
+            cta = begin * a.ctas / a.tokens;         // or one beside it
+            while (cta + 1 < a.ctas && first(cta + 1) <= begin) ++cta;
+            while (first(cta) > begin) --cta;
+        } else {
+            cta = y;
+            begin = first(cta + 1) / a.gate_tokens * a.gate_tokens;
+            if (begin == first(cta + 1) || begin < first(cta)) return;
+        }
+        const int64_t end = min(begin + a.gate_tokens, a.tokens);
+        if (cta + 1 == a.ctas || first(cta + 1) >= end) return;      // written by the CTA itself
+        // the first CTA's part lies in its second place unless the group is its first
+        if (col < dim) {
+            const float* p = a.gate_partial + col;
+            if (threadIdx.y == 0) s = p[(2 * cta + (first(cta) < begin)) * dim];
+            for (int64_t c = cta + 1 + threadIdx.y; c < a.ctas && first(c) < end; c += 16) s += p[2 * c * dim];
+        }
+        out = a.gate_out + begin / a.gate_tokens * dim;
+    }
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && col < dim) {
@@ -548,47 +957,6 @@ __device__ __forceinline__ void sum_columns(float s, int64_t col, int64_t dim, u
         for (int i = 1; i < 16; ++i) s += part[i][threadIdx.x];
         out[col] = float_to_bf16(s);
     }
-    __syncthreads();
-}
-
-__global__ void __launch_bounds__(512) norm_sum_kernel(const __grid_constant__ SumArgs a)
-{
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-    const float* p = a.partial + blockIdx.y * a.rows * a.dim + col;
-    float s = 0.0f;
-    if (col < a.dim) {
-#pragma unroll 4
-        for (int64_t r = threadIdx.y; r < a.rows; r += 16) s += p[r * a.dim];
-    }
-    sum_columns(s, col, a.dim, a.out[blockIdx.y]);
-}
-
-// The gradient of the gate of each group that more than one CTA has rows of: the
-// y index runs over the groups, or, where these are more, over the CTAs' ends.
-__global__ void __launch_bounds__(512) gate_sum_kernel(const float* partial, int64_t tokens, int64_t gate_tokens, int64_t ctas,
-                                                       int64_t dim, uint16_t* out)
-{
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-    const int64_t groups = (tokens + gate_tokens - 1) / gate_tokens;
-    int64_t begin, cta;                              // the group's first row, and the CTA that has it
-    if (groups < ctas) {
-        begin = blockIdx.y * gate_tokens;
-        cta = begin * ctas / tokens;                 // or one beside it
-        while (cta + 1 < ctas && first_row(tokens, cta + 1, ctas) <= begin) ++cta;
-        while (first_row(tokens, cta, ctas) > begin) --cta;
-    } else {
-        cta = blockIdx.y;
-        const int64_t next = first_row(tokens, cta + 1, ctas);
-        begin = next / gate_tokens * gate_tokens;
-        if (begin == next || begin < first_row(tokens, cta, ctas)) return;
-    }
-    const int64_t end = min(begin + gate_tokens, tokens);
-    if (cta + 1 == ctas || first_row(tokens, cta + 1, ctas) >= end) return;     // written by the CTA itself
-    float s = 0.0f;
-    if (col < dim)
-        for (int64_t c = cta + threadIdx.y; c < ctas && first_row(tokens, c, ctas) < end; c += 16)
-            s += partial[(2 * c + (first_row(tokens, c, ctas) < begin)) * dim + col];
-    sum_columns(s, col, dim, out + begin / gate_tokens * dim);
 }
 
 // ------------------------------------------------------------------------- host
@@ -606,6 +974,14 @@ bool vectors(const q8_block_norm& n)
     return ok;
 }
 
+bool backward_vectors(const q8_block_norm& n, const q8_block_norm_grads& g)
+{
+    const int64_t elem = n.residual_dtype == Q8_F32 ? 4 : 2;
+    return vectors(n) && on16(g.d_residual_out, g.d_residual_out ? g.d_residual_out_stride : 0, elem) &&
+           on16(g.dz, g.dz ? g.dz_stride : 0, 2) && on16(g.d_residual, g.d_residual ? g.d_residual_stride : 0, elem) &&
+           on16(g.d_y, g.d_y ? g.d_y_stride : 0, 2);
+}
+
 using ForwardKernel = void (*)(Forward);
 using BackwardKernel = void (*)(Backward);
 
@@ -620,9 +996,10 @@ Shape forward_shape(int64_t dim)
     return dim <= 4096 ? Shape{16, 256} : dim <= 8192 ? Shape{16, 512} : dim <= 16384 ? Shape{32, 512} : Shape{64, 512};
 }
 
-Shape backward_shape(int64_t dim)
+Shape backward_shape(int64_t dim, bool vec)
 {
-    return dim <= 4096 ? Shape{8, 512} : dim <= 8192 ? Shape{16, 512} : dim <= 16384 ? Shape{16, 1024} : Shape{32, 1024};
+    if (!vec && dim <= 4096) return Shape{8, 512};           // single elements take a register each
+    return dim <= 8192 ? Shape{16, 512} : dim <= 16384 ? Shape{16, 1024} : Shape{32, 1024};
 }
 
 int threads_of(int64_t dim, int elements) { return static_cast<int>(ceil_div(ceil_div(dim, elements), 32) * 32); }
@@ -636,13 +1013,14 @@ ForwardKernel forward_kernel(int64_t dim)
                             : s.elements == 32 ? norm_forward_kernel<R, VEC, 32, 512> : norm_forward_kernel<R, VEC, 64, 512>;
 }
 
-template <typename R, int VEC>
+template <typename R, int VEC, bool LAYER>
 BackwardKernel backward_kernel(int64_t dim)
 {
-    const Shape s = backward_shape(dim);
-    if (s.elements == 8) return norm_backward_kernel<R, VEC, 8, 512, 2>;
-    return s.most == 512 ? norm_backward_kernel<R, VEC, 16, 512, 1>
-                         : s.elements == 16 ? norm_backward_kernel<R, VEC, 16, 1024, 1> : norm_backward_kernel<R, VEC, 32, 1024, 1>;
+    const Shape s = backward_shape(dim, VEC == 8);
+    if constexpr (VEC == 1)
+        if (s.elements == 8) return norm_backward_kernel<R, VEC, 8, 512, LAYER>;
+    return s.most == 512 ? norm_backward_kernel<R, VEC, 16, 512, LAYER>
+                         : s.elements == 16 ? norm_backward_kernel<R, VEC, 16, 1024, LAYER> : norm_backward_kernel<R, VEC, 32, 1024, LAYER>;
 }
 
 ForwardKernel forward_kernel(bool f32, bool vec, int64_t dim)
@@ -651,36 +1029,66 @@ ForwardKernel forward_kernel(bool f32, bool vec, int64_t dim)
     return vec ? forward_kernel<uint16_t, 8>(dim) : forward_kernel<uint16_t, 1>(dim);
 }
 
-BackwardKernel backward_kernel(bool f32, bool vec, int64_t dim)
+BackwardKernel backward_kernel(bool f32, bool vec, bool layer, int64_t dim)
 {
-    if (f32) return vec ? backward_kernel<float, 8>(dim) : backward_kernel<float, 1>(dim);
-    return vec ? backward_kernel<uint16_t, 8>(dim) : backward_kernel<uint16_t, 1>(dim);
+    if (f32)
+        return vec ? (layer ? backward_kernel<float, 8, true>(dim) : backward_kernel<float, 8, false>(dim))
+                   : (layer ? backward_kernel<float, 1, true>(dim) : backward_kernel<float, 1, false>(dim));
+    return vec ? (layer ? backward_kernel<uint16_t, 8, true>(dim) : backward_kernel<uint16_t, 8, false>(dim))
+               : (layer ? backward_kernel<uint16_t, 1, true>(dim) : backward_kernel<uint16_t, 1, false>(dim));
 }
 
-// CTAs of the backward kernel: a function of sizes alone, for the workspace is
-// sized by it; as many as are resident where their sums lie in shared memory.
-constexpr int64_t kSums227 = 227 * 1024 - 1024;
+// The staged kernel: rows up to 4096 columns in CTAs of which an SM holds two or
+// more, up to 8192 in one.
+template <typename R>
+BackwardKernel staged_kernel(bool layer, int threads)
+{
+    if (threads <= 512) return layer ? norm_staged_kernel<R, true, 512, 2> : norm_staged_kernel<R, false, 512, 2>;
+    return layer ? norm_staged_kernel<R, true, 1024, 1> : norm_staged_kernel<R, false, 1024, 1>;
+}
+
+BackwardKernel staged_kernel(bool f32, bool layer, int threads)
+{
+    return f32 ? staged_kernel<float>(layer, threads) : staged_kernel<uint16_t>(layer, threads);
+}
+
+// What the backward kernel does: a function of sizes, strides and pointers
+// alone, for the workspace is sized by it.  As many CTAs as are resident.
+constexpr int64_t kMostShared = 227 * 1024 - 1024;
 
 struct Plan {
     int64_t ctas, span;              // span: columns of a sum as the CTA keeps it
     int threads, wanted, at[kSums];
-    bool shared;
+    bool staged, vec, shared;        // shared: the sums lie in shared memory
     int64_t smem, partial, gate_partial, scratch, bytes;
 };
 
 Plan plan(const q8_block_norm& n, const q8_block_norm_grads& g, int sms)
 {
     Plan p{};
-    const Shape s = backward_shape(n.dim);
-    p.threads = threads_of(n.dim, s.elements);
-    p.span = static_cast<int64_t>(p.threads) * s.elements;
     const uint16_t* outs[kSums] = {g.d_post_weight, g.d_post_bias, g.d_pre_weight, g.d_pre_bias, g.d_gate};
     for (int i = 0; i < kSums; ++i) p.at[i] = outs[i] ? p.wanted++ : -1;
-    p.smem = p.wanted * p.span * 4;
-    p.shared = p.smem <= kSums227;
-    const int64_t by_threads = std::max(1, (s.elements == 8 ? 1024 : s.most) / p.threads);
-    const int64_t by_smem = p.shared && p.smem ? std::max<int64_t>(1, 227 * 1024 / (p.smem + 2048)) : by_threads;
-    p.ctas = std::min<int64_t>(n.tokens, sms * std::min<int64_t>(16, std::min(by_threads, by_smem)));
+    p.vec = backward_vectors(n, g);
+    const int64_t stages = 2 * n.dim * (4 + 2 * (n.residual_dtype == Q8_F32 ? 4 : 2));
+    int64_t resident;                                        // CTAs to an SM, by their threads
+    p.threads = threads_of(n.dim, 8);
+    p.span = p.threads * int64_t(8);
+    p.smem = p.wanted * p.span * 4 + stages;
+    p.staged = p.vec && p.threads <= 1024 && p.smem <= kMostShared;
+    if (p.staged) {
+        resident = 1024 / p.threads;
+        p.shared = true;
+    } else {
+        const Shape s = backward_shape(n.dim, p.vec);
+        p.threads = threads_of(n.dim, s.elements);
+        p.span = static_cast<int64_t>(p.threads) * s.elements;
+        p.smem = p.wanted * p.span * 4;
+        p.shared = p.smem <= kMostShared;
+        if (!p.shared) p.smem = 0;
+        resident = std::max(1, s.most / p.threads);
+    }
+    resident = std::min<int64_t>({resident, 16, 228 * 1024 / (p.smem + 2048)});
+    p.ctas = std::min<int64_t>({n.tokens, kMostCtas, sms * std::max<int64_t>(1, resident)});
     auto take = [&](int64_t floats) {
         const int64_t at = p.bytes;
         p.bytes += ceil_div(floats * 4, 256) * 256;
@@ -712,9 +1120,14 @@ cudaError_t prepare_norm()
                 const Shape s = forward_shape(dim);
                 if (e == cudaSuccess)
                     e = persistent_grid(reinterpret_cast<const void*>(forward_kernel(f32, vec, dim)), s.most, 0, &grid);
-                if (e == cudaSuccess)
-                    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(backward_kernel(f32, vec, dim)),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSums227);
+                for (bool layer : {false, true}) {
+                    if (e == cudaSuccess)
+                        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(staged_kernel(f32, layer, dim <= 4096 ? 512 : 1024)),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+                    if (e == cudaSuccess)
+                        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(backward_kernel(f32, vec, layer, dim)),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+                }
             }
     return e;
 }
@@ -743,11 +1156,11 @@ int64_t norm_workspace(const q8_block_norm& n, const q8_block_norm_grads& g)
 cudaError_t launch_norm_backward(const q8_block_norm& n, const q8_block_norm_grads& g, cudaStream_t st)
 {
     const bool f32 = n.residual_dtype == Q8_F32;
-    const int64_t elem = f32 ? 4 : 2;
-    const bool vec = vectors(n) && on16(g.d_residual_out, g.d_residual_out ? g.d_residual_out_stride : 0, elem) &&
-                     on16(g.dz, g.dz ? g.dz_stride : 0, 2) && on16(g.d_residual, g.d_residual ? g.d_residual_stride : 0, elem) &&
-                     on16(g.d_y, g.d_y ? g.d_y_stride : 0, 2);
-    const Plan p = plan(n, g, sm_count());
+    DeviceInfo dev;
+    cudaError_t e = device_info(&dev);
+    if (e == cudaSuccess) e = earlier_fault(dev.fault);
+    if (e != cudaSuccess) return e;
+    const Plan p = plan(n, g, dev.sms);
     uint8_t* ws = static_cast<uint8_t*>(g.workspace);
     Backward a{};
     a.n = n;
@@ -757,24 +1170,22 @@ cudaError_t launch_norm_backward(const q8_block_norm& n, const q8_block_norm_gra
     a.scratch = p.shared ? nullptr : reinterpret_cast<float*>(ws + p.scratch);
     a.wanted = p.wanted;
     for (int i = 0; i < kSums; ++i) a.at[i] = p.at[i];
-    const BackwardKernel k = backward_kernel(f32, vec, n.dim);
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, kSums227);
+    a.fault = dev.fault;
+    const bool layer = n.post_kind == Q8_NORM_LAYER || n.pre_kind == Q8_NORM_LAYER;
+    const BackwardKernel k = p.staged ? staged_kernel(f32, layer, p.threads) : backward_kernel(f32, p.vec, layer, n.dim);
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e != cudaSuccess) return e;
-    k<<<static_cast<unsigned>(p.ctas), p.threads, p.shared ? static_cast<size_t>(p.smem) : 0, st>>>(a);
+    k<<<static_cast<unsigned>(p.ctas), p.threads, static_cast<size_t>(p.smem), st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const unsigned blocks = static_cast<unsigned>(ceil_div(n.dim, 32));
-    SumArgs s{a.partial, {}, p.ctas, n.dim};
+    SumArgs s{a.partial, a.gate_partial, {}, g.d_gate, p.ctas, n.dim, n.tokens, std::max<int64_t>(1, n.gate_tokens), 0};
     uint16_t* outs[kGate] = {g.d_post_weight, g.d_post_bias, g.d_pre_weight, g.d_pre_bias};
-    int count = 0;
     for (uint16_t* o : outs)
-        if (o) s.out[count++] = o;
-    if (count) norm_sum_kernel<<<dim3(blocks, count), dim3(32, 16), 0, st>>>(s);
-    if (g.d_gate && p.ctas > 1) {
-        // only groups that reach from one CTA into the next have anything to add
-        const int64_t groups = ceil_div(n.tokens, n.gate_tokens);
-        gate_sum_kernel<<<dim3(blocks, static_cast<unsigned>(groups < p.ctas ? groups : p.ctas - 1)), dim3(32, 16), 0, st>>>(
-            a.gate_partial, n.tokens, n.gate_tokens, p.ctas, n.dim, g.d_gate);
-    }
+        if (o) s.out[s.count++] = o;
+    int64_t ends = 0;                                        // of the gate's groups that may reach over two CTAs
+    if (g.d_gate && p.ctas > 1) ends = std::min(ceil_div(n.tokens, n.gate_tokens), p.ctas - 1);
+    if (s.count + ends > 0)
+        norm_sum_kernel<<<dim3(static_cast<unsigned>(ceil_div(n.dim, 32)), static_cast<unsigned>(s.count + ends)), dim3(32, 16), 0,
+                          st>>>(s);
     return cudaGetLastError();
 }
 
