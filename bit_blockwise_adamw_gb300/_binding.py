@@ -7,6 +7,7 @@ is no fallback path.
 """
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -76,32 +77,14 @@ class _Tensor16(C.Structure):
                 ("v", C.c_void_p), ("numel", C.c_int64), ("philox_offset", C.c_int64)]
 
 
-_P, _I64 = C.c_void_p, C.c_int64
-
-
-class _GatedFF(C.Structure):
-    _fields_ = [("x", _P), ("w_gate", _P), ("w_up", _P), ("tokens", _I64), ("d_model", _I64), ("d_ff", _I64),
-                ("x_stride", _I64), ("workspace", _P), ("workspace_bytes", _I64), ("act", C.c_int32)]
-
-
-class _BlockNorm(C.Structure):
-    _fields_ = [("residual", _P), ("y", _P), ("post_weight", _P), ("post_bias", _P), ("pre_weight", _P),
-                ("pre_bias", _P), ("gate", _P), ("tokens", _I64), ("dim", _I64), ("gate_tokens", _I64),
-                ("residual_stride", _I64), ("y_stride", _I64), ("post_kind", C.c_int32), ("pre_kind", C.c_int32),
-                ("residual_dtype", C.c_int32), ("eps", C.c_float), ("residual_scale", C.c_float)]
-
-
-class _BlockNormGrads(C.Structure):
-    _fields_ = [("d_residual_out", _P), ("dz", _P), ("d_residual", _P), ("d_y", _P), ("d_post_weight", _P),
-                ("d_post_bias", _P), ("d_pre_weight", _P), ("d_pre_bias", _P), ("d_gate", _P),
-                ("d_residual_out_stride", _I64), ("dz_stride", _I64), ("d_residual_stride", _I64),
-                ("d_y_stride", _I64), ("workspace", _P), ("workspace_bytes", _I64)]
-
-
-class _DistillTopk(C.Structure):
-    _fields_ = [("logits", _P), ("teacher_ids", _P), ("teacher_logits", _P), ("labels", _P), ("row_weight", _P),
-                ("rows", _I64), ("vocab", _I64), ("k", _I64), ("logits_stride", _I64), ("logits_dtype", C.c_int32),
-                ("temperature", C.c_float), ("kd_weight", C.c_float), ("ce_weight", C.c_float)]
+# The argument structures of include/q8train.h.  These calls are short, and what
+# goes before the launch is a good part of the smallest ones: their structures
+# are packed as bytes (native alignment, as the C compiler lays them out), which
+# takes half the time of filling a ctypes.Structure.
+_GATED_FF = struct.Struct("PPPqqqqPqi4x")
+_BLOCK_NORM = struct.Struct("PPPPPPPqqqqqiiiff4x")
+_BLOCK_NORM_GRADS = struct.Struct("PPPPPPPPPqqqqPq")
+_DISTILL_TOPK = struct.Struct("PPPPPqqqqifff")
 
 
 _lib = None
@@ -134,7 +117,7 @@ def load_library(path: Optional[str] = None):
     L.q8_last_error.argtypes = []
     L.q8_last_error.restype = C.c_char_p
     L.q8_abi_version.argtypes = []
-    # the structures go as addresses (c_void_p): ctypes.byref is accepted
+    # the structures go as the addresses of their bytes
     L.q8_gated_ff_workspace.argtypes = [P, C.c_int]
     L.q8_gated_ff_forward.argtypes = [P, P, C.c_int64, P, S]
     L.q8_gated_ff_backward.argtypes = [P, P, C.c_int64, P, P, C.c_int64, P, P, S]
@@ -348,65 +331,80 @@ def lion8bit_sr_step(tensors, hp: LionHParams, stream=None) -> None:
 
 # ------------------------------------------------- training-step operators
 
-def _rows(t: torch.Tensor, name: str, dtype, cols=None, rows=None):
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
+_DTYPES = {_BF: 0, _F32: 1}                          # q8_dtype
+
+
+def _on(stream, t):
+    """The stream's address: the given one, or the current one of t's device."""
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape):
     """(address, row stride) of a [rows, cols] matrix whose rows are contiguous."""
-    shape = t.shape
-    if t.dtype != dtype or not t.is_cuda or len(shape) != 2 or (cols is not None and shape[1] != cols) or \
-            (rows is not None and shape[0] != rows):
-        raise ValueError("%s must be a %s CUDA matrix%s" % (name, dtype, "" if cols is None else " of the matching size"))
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape:
+        raise ValueError("%s must be a %s CUDA matrix of shape %s" % (name, dtype, tuple(shape)))
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     row, col = t.stride()
     if col != 1 and shape[1] != 1:
         raise ValueError("%s's rows must be contiguous" % name)
     return t.data_ptr(), row if shape[0] > 1 else shape[1]
 
 
+def _first(t: torch.Tensor, name: str, dtype):
+    """_rows of the matrix that the others' sizes follow from."""
+    if t.dim() != 2:
+        raise ValueError("%s must be a %s CUDA matrix" % (name, dtype))
+    return _rows(t, name, dtype, t.shape)
+
+
 def _array(t: Optional[torch.Tensor], name: str, dtype, shape):
-    """Address of a contiguous array of that type and shape, or None."""
+    """Address of a contiguous array of that type and shape, or 0."""
     if t is None:
-        return None
-    if t.dtype != dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        return 0
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s CUDA array of shape %s" % (name, dtype, tuple(shape)))
     return t.data_ptr()
 
 
-def _opt_rows(t, name, dtype, cols, rows):
-    return (None, 0) if t is None else _rows(t, name, dtype, cols, rows)
-
-
-def _workspace(fn, bytes_, workspace, device, stream):
+def _workspace(fn, need, workspace, like, stream):
     """(address, bytes, the tensor that holds it): the caller's workspace, or
     one from torch's allocator for the stream that the call runs on."""
-    if bytes_ < 0:
-        _check(fn, bytes_)
+    if need < 0:
+        _check(fn, need)
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    if bytes_ == 0:
-        return None, 0, None
+    if need == 0:
+        return 0, 0, None
     if stream is None:
-        t = torch.empty(bytes_, dtype=torch.uint8, device=device)
+        t = torch.empty(need, dtype=torch.uint8, device=like.device)
     else:
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
-                torch.cuda.default_stream(device)
+            stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else \
+                torch.cuda.default_stream(like.device)
         with torch.cuda.stream(stream):
-            t = torch.empty(bytes_, dtype=torch.uint8, device=device)
-    return t.data_ptr(), bytes_, t
+            t = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return t.data_ptr(), need, t
 
 
 def _gated_ff(x, w_gate, w_up, act):
-    xp, xs = _rows(x, "x", torch.bfloat16)
+    xp, xs = _first(x, "x", _BF)
     tokens, d_model = x.shape
     d_ff = w_gate.shape[0]
-    wg = _array(w_gate, "w_gate", torch.bfloat16, (d_ff, d_model))
-    wu = _array(w_up, "w_up", torch.bfloat16, (d_ff, d_model))
-    return _GatedFF(xp, wg, wu, tokens, d_model, d_ff, xs, None, 0, act)
+    shape = (d_ff, d_model)
+    return (xp, _array(w_gate, "w_gate", _BF, shape), _array(w_up, "w_up", _BF, shape), tokens, d_model, d_ff, xs), act
 
 
 def q8_gated_ff_workspace(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, backward=False) -> int:
     """Bytes of workspace of q8_gated_ff_forward (backward: of ..._backward)."""
-    n = load_library().q8_gated_ff_workspace(C.byref(_gated_ff(x, w_gate, w_up, SILU)), int(backward))
+    f, act = _gated_ff(x, w_gate, w_up, SILU)
+    n = load_library().q8_gated_ff_workspace(_GATED_FF.pack(*f, 0, 0, act), int(backward))
     if n < 0:
         _check("q8_gated_ff_workspace", n)
     return n
@@ -418,13 +416,16 @@ def q8_gated_ff_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tenso
     """h = act(x w_gate^T) * (x w_up^T); saved: float32 [2, tokens, d_ff] that
     receives both projections for the backward call.  Without a workspace the
     binding allocates one (from torch's caching allocator) where it is needed."""
-    L = load_library()
-    f = _gated_ff(x, w_gate, w_up, act)
-    hp, hs = _rows(h, "h", torch.bfloat16, f.d_ff, f.tokens)
-    sp = _array(saved, "saved", torch.float32, (2, f.tokens, f.d_ff))
-    need = L.q8_gated_ff_workspace(C.byref(f), 0)
-    f.workspace, f.workspace_bytes, keep = _workspace("q8_gated_ff_forward", need, workspace, x.device, stream)
-    _check("q8_gated_ff_forward", L.q8_gated_ff_forward(C.byref(f), hp, hs, sp, _stream(stream)))
+    L = _lib or load_library()
+    f, act = _gated_ff(x, w_gate, w_up, act)
+    tokens, d_ff = f[3], f[5]
+    hp, hs = _rows(h, "h", _BF, (tokens, d_ff))
+    sp = _array(saved, "saved", _F32, (2, tokens, d_ff))
+    need = L.q8_gated_ff_workspace(_GATED_FF.pack(*f, 0, 0, act), 0)
+    wp, wb, keep = (0, 0, None) if need == 0 else _workspace("q8_gated_ff_forward", need, workspace, x, stream)
+    rc = L.q8_gated_ff_forward(_GATED_FF.pack(*f, wp, wb, act), hp, hs, sp, _on(stream, x))
+    if rc:
+        _check("q8_gated_ff_forward", rc)
 
 
 def q8_gated_ff_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dh: torch.Tensor,
@@ -433,19 +434,19 @@ def q8_gated_ff_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
                          workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """dx, dw_gate, dw_up (each may be None) from dh; saved as the forward call
     wrote it, or None to compute both projections again."""
-    L = load_library()
-    f = _gated_ff(x, w_gate, w_up, act)
-    dhp, dhs = _rows(dh, "dh", torch.bfloat16, f.d_ff, f.tokens)
-    sp = _array(saved, "saved", torch.float32, (2, f.tokens, f.d_ff))
-    dxp, dxs = _opt_rows(dx, "dx", torch.bfloat16, f.d_model, f.tokens)
-    gp = _array(dw_gate, "dw_gate", torch.bfloat16, w_gate.shape)
-    up = _array(dw_up, "dw_up", torch.bfloat16, w_up.shape)
-    need = L.q8_gated_ff_workspace(C.byref(f), 1)
-    f.workspace, f.workspace_bytes, keep = _workspace("q8_gated_ff_backward", need, workspace, x.device, stream)
-    _check("q8_gated_ff_backward", L.q8_gated_ff_backward(C.byref(f), dhp, dhs, sp, dxp, dxs, gp, up, _stream(stream)))
-
-
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1}     # q8_dtype
+    L = _lib or load_library()
+    f, act = _gated_ff(x, w_gate, w_up, act)
+    tokens, d_model, d_ff = f[3:6]
+    dhp, dhs = _rows(dh, "dh", _BF, (tokens, d_ff))
+    sp = _array(saved, "saved", _F32, (2, tokens, d_ff))
+    dxp, dxs = (0, 0) if dx is None else _rows(dx, "dx", _BF, (tokens, d_model))
+    gp = _array(dw_gate, "dw_gate", _BF, (d_ff, d_model))
+    up = _array(dw_up, "dw_up", _BF, (d_ff, d_model))
+    need = L.q8_gated_ff_workspace(_GATED_FF.pack(*f, 0, 0, act), 1)
+    wp, wb, keep = _workspace("q8_gated_ff_backward", need, workspace, x, stream)
+    rc = L.q8_gated_ff_backward(_GATED_FF.pack(*f, wp, wb, act), dhp, dhs, sp, dxp, dxs, gp, up, _on(stream, x))
+    if rc:
+        _check("q8_gated_ff_backward", rc)
 
 
 def _dtype(t, name):
@@ -457,24 +458,28 @@ def _dtype(t, name):
 
 def _block_norm(residual, y, post_kind, pre_kind, post_weight, post_bias, pre_weight, pre_bias, gate, gate_tokens,
                 residual_scale, eps):
-    bf = torch.bfloat16
-    yp, ys = _rows(y, "y", bf)
-    tokens, dim = y.shape
-    rp, rs = _rows(residual, "residual", residual.dtype, dim, tokens)
+    yp, ys = _first(y, "y", _BF)
+    shape = y.shape
+    tokens, dim = shape
+    dtype = _dtype(residual, "residual")
+    rp, rs = _rows(residual, "residual", residual.dtype, shape)
     vec = (dim,)
-    gp = None
+    gp = 0
     if gate is not None:
-        rows = gate.numel() // dim
+        if gate.dim() == 1:
+            rows, gp = 1, _array(gate, "gate", _BF, vec)
+        else:
+            rows = gate.shape[0]
+            gp = _array(gate, "gate", _BF, (rows, dim))
         if gate_tokens is None:
             if rows < 1 or tokens % rows:
                 raise ValueError("gate's rows must divide the tokens (or give gate_tokens)")
             gate_tokens = max(1, tokens // rows)
         elif gate_tokens > 0 and rows < -(-tokens // gate_tokens):
             raise ValueError("gate has fewer rows than ceil(tokens / gate_tokens)")
-        gp = _array(gate, "gate", bf, vec if gate.dim() == 1 else (rows, dim))
-    return _BlockNorm(rp, yp, _array(post_weight, "post_weight", bf, vec), _array(post_bias, "post_bias", bf, vec),
-                      _array(pre_weight, "pre_weight", bf, vec), _array(pre_bias, "pre_bias", bf, vec), gp, tokens, dim,
-                      gate_tokens or 0, rs, ys, post_kind, pre_kind, _dtype(residual, "residual"), eps, residual_scale)
+    return _BLOCK_NORM.pack(rp, yp, _array(post_weight, "post_weight", _BF, vec), _array(post_bias, "post_bias", _BF, vec),
+                            _array(pre_weight, "pre_weight", _BF, vec), _array(pre_bias, "pre_bias", _BF, vec), gp,
+                            tokens, dim, gate_tokens or 0, rs, ys, post_kind, pre_kind, dtype, eps, residual_scale)
 
 
 def q8_block_norm_forward(residual: torch.Tensor, y: torch.Tensor, residual_out: Optional[torch.Tensor],
@@ -484,12 +489,15 @@ def q8_block_norm_forward(residual: torch.Tensor, y: torch.Tensor, residual_out:
     """residual_out = residual_scale * residual + gate * N_post(y) and
     z = N_pre(residual_out).  gate: [dim] or [rows, dim], a row for each
     gate_tokens consecutive tokens (by default tokens / rows)."""
+    L = _lib or load_library()
     n = _block_norm(residual, y, post_kind, pre_kind, post_weight, post_bias, pre_weight, pre_bias, gate, gate_tokens,
                     residual_scale, eps)
-    op, os_ = _opt_rows(residual_out, "residual_out", residual.dtype, n.dim, n.tokens)
-    zp, zs = _opt_rows(z, "z", torch.bfloat16, n.dim, n.tokens)
-    _check("q8_block_norm_forward",
-           load_library().q8_block_norm_forward(C.byref(n), op, os_, zp, zs, _stream(stream)))
+    shape = y.shape
+    op, os_ = (0, 0) if residual_out is None else _rows(residual_out, "residual_out", residual.dtype, shape)
+    zp, zs = (0, 0) if z is None else _rows(z, "z", _BF, shape)
+    rc = L.q8_block_norm_forward(n, op, os_, zp, zs, _on(stream, y))
+    if rc:
+        _check("q8_block_norm_forward", rc)
 
 
 def q8_block_norm_backward(residual: torch.Tensor, y: torch.Tensor, dresidual_out: Optional[torch.Tensor],
@@ -501,34 +509,37 @@ def q8_block_norm_backward(residual: torch.Tensor, y: torch.Tensor, dresidual_ou
                            workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """The gradients of q8_block_norm_forward's inputs (each output may be
     None) from those of its outputs (None: zeros)."""
-    L = load_library()
+    L = _lib or load_library()
     n = _block_norm(residual, y, post_kind, pre_kind, post_weight, post_bias, pre_weight, pre_bias, gate, gate_tokens,
                     residual_scale, eps)
-    bf, vec = torch.bfloat16, (n.dim,)
-    rop, ros = _opt_rows(dresidual_out, "dresidual_out", residual.dtype, n.dim, n.tokens)
-    dzp, dzs = _opt_rows(dz, "dz", bf, n.dim, n.tokens)
-    drp, drs = _opt_rows(dresidual, "dresidual", residual.dtype, n.dim, n.tokens)
-    dyp, dys = _opt_rows(dy, "dy", bf, n.dim, n.tokens)
+    shape, dtype = y.shape, residual.dtype
+    vec = (shape[1],)
+    rop, ros = (0, 0) if dresidual_out is None else _rows(dresidual_out, "dresidual_out", dtype, shape)
+    dzp, dzs = (0, 0) if dz is None else _rows(dz, "dz", _BF, shape)
+    drp, drs = (0, 0) if dresidual is None else _rows(dresidual, "dresidual", dtype, shape)
+    dyp, dys = (0, 0) if dy is None else _rows(dy, "dy", _BF, shape)
     if dgate is not None and gate is None:
         raise ValueError("dgate without a gate")
-    g = _BlockNormGrads(rop, dzp, drp, dyp, _array(dpost_weight, "dpost_weight", bf, vec),
-                        _array(dpost_bias, "dpost_bias", bf, vec), _array(dpre_weight, "dpre_weight", bf, vec),
-                        _array(dpre_bias, "dpre_bias", bf, vec),
-                        None if dgate is None else _array(dgate, "dgate", bf, gate.shape), ros, dzs, drs, dys, None, 0)
-    need = L.q8_block_norm_workspace(C.byref(n), C.byref(g))
-    g.workspace, g.workspace_bytes, keep = _workspace("q8_block_norm_backward", need, workspace, y.device, stream)
-    _check("q8_block_norm_backward", L.q8_block_norm_backward(C.byref(n), C.byref(g), _stream(stream)))
+    g = (rop, dzp, drp, dyp, _array(dpost_weight, "dpost_weight", _BF, vec), _array(dpost_bias, "dpost_bias", _BF, vec),
+         _array(dpre_weight, "dpre_weight", _BF, vec), _array(dpre_bias, "dpre_bias", _BF, vec),
+         0 if dgate is None else _array(dgate, "dgate", _BF, gate.shape), ros, dzs, drs, dys)
+    need = L.q8_block_norm_workspace(n, _BLOCK_NORM_GRADS.pack(*g, 0, 0))
+    wp, wb, keep = _workspace("q8_block_norm_backward", need, workspace, y, stream)
+    rc = L.q8_block_norm_backward(n, _BLOCK_NORM_GRADS.pack(*g, wp, wb), _on(stream, y))
+    if rc:
+        _check("q8_block_norm_backward", rc)
 
 
 def _distill(logits, teacher_ids, teacher_logits, labels, row_weight, temperature, kd_weight, ce_weight):
-    zp, zs = _rows(logits, "logits", logits.dtype)
+    dtype = _dtype(logits, "logits")
+    zp, zs = _first(logits, "logits", logits.dtype)
     rows, vocab = logits.shape
     k = teacher_ids.shape[1] if teacher_ids is not None else 0
-    return _DistillTopk(zp, _array(teacher_ids, "teacher_ids", torch.int64, (rows, k)),
-                        _array(teacher_logits, "teacher_logits", torch.float32, (rows, k)),
-                        _array(labels, "labels", torch.int64, (rows,)),
-                        _array(row_weight, "row_weight", torch.float32, (rows,)), rows, vocab, k, zs,
-                        _dtype(logits, "logits"), temperature, kd_weight, ce_weight)
+    vec = (rows,)
+    return _DISTILL_TOPK.pack(zp, _array(teacher_ids, "teacher_ids", _I64, (rows, k)),
+                              _array(teacher_logits, "teacher_logits", _F32, (rows, k)),
+                              _array(labels, "labels", _I64, vec), _array(row_weight, "row_weight", _F32, vec),
+                              rows, vocab, k, zs, dtype, temperature, kd_weight, ce_weight)
 
 
 def q8_distill_topk_forward(logits: torch.Tensor, teacher_ids: Optional[torch.Tensor],
@@ -540,12 +551,15 @@ def q8_distill_topk_forward(logits: torch.Tensor, teacher_ids: Optional[torch.Te
     """Each row's distillation loss (float32 [rows]); stats: float32 [rows, 2]
     for the backward call; dlogits: the gradient of sum(row_weight * loss) in
     the same pass (it may be the logits themselves)."""
+    L = _lib or load_library()
     d = _distill(logits, teacher_ids, teacher_logits, labels, row_weight, temperature, kd_weight, ce_weight)
-    lp = _array(loss, "loss", torch.float32, (d.rows,))
-    sp = _array(stats, "stats", torch.float32, (d.rows, 2))
-    gp, gs = _opt_rows(dlogits, "dlogits", logits.dtype, d.vocab, d.rows)
-    _check("q8_distill_topk_forward",
-           load_library().q8_distill_topk_forward(C.byref(d), lp, sp, gp, gs, _stream(stream)))
+    rows = logits.shape[0]
+    lp = _array(loss, "loss", _F32, (rows,))
+    sp = _array(stats, "stats", _F32, (rows, 2))
+    gp, gs = (0, 0) if dlogits is None else _rows(dlogits, "dlogits", logits.dtype, logits.shape)
+    rc = L.q8_distill_topk_forward(d, lp, sp, gp, gs, _on(stream, logits))
+    if rc:
+        _check("q8_distill_topk_forward", rc)
 
 
 def q8_distill_topk_backward(logits: torch.Tensor, teacher_ids: Optional[torch.Tensor],
@@ -555,8 +569,10 @@ def q8_distill_topk_backward(logits: torch.Tensor, teacher_ids: Optional[torch.T
                              stream=None) -> None:
     """The logits' gradient from the forward call's stats; row_weight: the
     gradient of the losses."""
+    L = _lib or load_library()
     d = _distill(logits, teacher_ids, teacher_logits, labels, row_weight, temperature, kd_weight, ce_weight)
-    sp = _array(stats, "stats", torch.float32, (d.rows, 2))
-    gp, gs = _rows(dlogits, "dlogits", logits.dtype, d.vocab, d.rows)
-    _check("q8_distill_topk_backward",
-           load_library().q8_distill_topk_backward(C.byref(d), sp, gp, gs, _stream(stream)))
+    sp = _array(stats, "stats", _F32, (logits.shape[0], 2))
+    gp, gs = _rows(dlogits, "dlogits", logits.dtype, logits.shape)
+    rc = L.q8_distill_topk_backward(d, sp, gp, gs, _on(stream, logits))
+    if rc:
+        _check("q8_distill_topk_backward", rc)

@@ -359,6 +359,135 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     if (warp == 1) tmem_free_all(tmem);
 }
 
+// ------------------------------------------------------------ few tokens
+//
+// Up to 128 tokens the weights' bytes bound the forward product.  The weights
+// are the tensor core's M then (64 rows of w_gate over the same 64 of w_up: one
+// 128-row tile), the tokens its N, padded to 16, 32, 64 or 128 instead of 256;
+// a CTA has a tile, and two CTAs on an SM keep 200 KB of weights in flight.
+// A lane of tensor memory is a column of h: lanes 64..127 pass u through shared
+// memory to lanes 0..63.
+constexpr int kFewTokens = 128, kFewRows = 64, kFewThreads = 128, kFewStages = 8;
+
+struct FewArgs {
+    CUtensorMap x, w[2];
+    int32_t tokens, columns, stages, k_steps;        // columns: the padded tokens
+    int64_t d_ff;
+    uint16_t* h;
+    int64_t h_stride;
+    float* save;
+    int32_t act;
+    int32_t* fault;
+};
+
+constexpr int kFewSmem = 112 * 1024;                 // two CTAs on an SM
+
+int few_stage_bytes(int columns) { return kOperandBytes + columns * kStepK * 2; }
+
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewArgs args)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t s_bar[2 * kFewStages + 1];
+    __shared__ uint32_t s_tmem;
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    const uint32_t stage_bytes = kOperandBytes + args.columns * kStepK * 2;
+    const auto full = [&](int s) { return smem_addr(&s_bar[s]); };
+    const auto empty = [&](int s) { return smem_addr(&s_bar[kFewStages + s]); };
+    const uint32_t done = smem_addr(&s_bar[2 * kFewStages]);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int f0 = blockIdx.x * kFewRows;
+    const uint32_t tmem_columns = max(32, args.columns);
+
+    if (warp == 0 && elect()) {
+        for (int s = 0; s < kFewStages; ++s) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        bar_init(done, 1);
+        bar_init_fence();
+    }
+    if (warp == 1) tmem_alloc_single(smem_addr(&s_tmem), tmem_columns);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    bool ok = true;
+    if (warp == 0 && elect()) {
+        int s = 0;
+        uint32_t phase = 1;
+        for (int k = 0; k < args.k_steps; ++k) {
+            if (!(ok = bar_wait(empty(s), phase))) break;
+            bar_expect(full(s), stage_bytes);
+            const uint32_t sa = base + s * stage_bytes;
+            tma_load_single(sa, &args.w[0], k * kStepK, f0, full(s));
+            tma_load_single(sa + kOperandBytes / 2, &args.w[1], k * kStepK, f0, full(s));
+            tma_load_single(sa + kOperandBytes, &args.x, k * kStepK, 0, full(s));
+            if (++s == args.stages) s = 0, phase ^= 1;
+        }
+        // every load's stage has been given back before the CTA ends
+        for (int i = 0; i < args.stages; ++i) {
+            ok = bar_wait(empty(s), phase) && ok;
+            if (++s == args.stages) s = 0, phase ^= 1;
+        }
+    } else if (warp == 1 && elect()) {
+        const uint32_t desc = mma_desc(false, false, 128, args.columns);
+        int s = 0;
+        uint32_t phase = 0;
+        for (int k = 0; k < args.k_steps; ++k) {
+            if (!(ok = bar_wait(full(s), phase))) break;
+            tc_fence_after();
+            const uint32_t sa = base + s * stage_bytes, sb = sa + kOperandBytes;
+#pragma unroll
+            for (int j = 0; j < kStepK / 16; ++j)
+                mma_single(tmem, smem_desc(sa + j * 32, 16, 1024), smem_desc(sb + j * 32, 16, 1024), desc, k > 0 || j > 0);
+            mma_commit_single(empty(s));
+            if (++s == args.stages) s = 0, phase ^= 1;
+        }
+        mma_commit_single(done);
+    }
+    __syncwarp();
+    ok = __all_sync(0xFFFFFFFFu, bar_wait(done, 0)) && ok;
+    tc_fence_after();
+
+    // lane l < 64: column f0 + l of g; lane 64 + l: the same of u
+    const int l = (warp & 1) * 32 + lane;
+    const int64_t f = static_cast<int64_t>(f0) + l;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    float* s_u = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));      // [columns][64], over the stages
+    __syncthreads();                                 // which nobody reads any more
+    float v[16];
+    if (warp >= 2) {
+        for (int c = 0; c < args.columns; c += 16) {
+            tmem_load16(lanes + c, v);
+            tmem_load_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                s_u[(c + j) * kFewRows + l] = v[j];
+                if (args.save && c + j < args.tokens && f < args.d_ff)
+                    args.save[(static_cast<int64_t>(args.tokens) + c + j) * args.d_ff + f] = v[j];
+            }
+        }
+    }
+    __syncthreads();
+    if (warp < 2) {
+        for (int c = 0; c < args.columns; c += 16) {
+            tmem_load16(lanes + c, v);
+            tmem_load_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (c + j >= args.tokens || f >= args.d_ff) continue;
+                if (args.save) args.save[static_cast<int64_t>(c + j) * args.d_ff + f] = v[j];
+                args.h[(c + j) * args.h_stride + f] = float_to_bf16(act_value(v[j], args.act) * s_u[(c + j) * kFewRows + l]);
+            }
+        }
+    }
+    if (!ok) atomicExch_system(args.fault, 1);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free_single(tmem, tmem_columns);
+}
+
 // out = the sum of the splits' parts, in their order.
 __global__ void __launch_bounds__(256) join_kernel(const float* partial, int splits, int64_t M, int64_t N, uint16_t* out,
                                                    int64_t out_stride)
@@ -503,6 +632,7 @@ cudaError_t device(Device* out)
             reinterpret_cast<const void*>(tile_kernel<kInput>), reinterpret_cast<const void*>(tile_kernel<kWeight>)};
         for (const void* k : kernels)
             if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem)) != cudaSuccess) return e;
         d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
     *out = d;
@@ -626,6 +756,26 @@ cudaError_t launch_ff_forward(const q8_gated_ff& f, uint16_t* h, int64_t h_strid
     const Layout l = layout(f, false, pairs_of(d));
     Matrix m[3];
     if ((e = operands(f, l, d, st, m)) != cudaSuccess) return e;
+    if (f.tokens <= kFewTokens) {
+        FewArgs a{};
+        a.tokens = static_cast<int32_t>(f.tokens);
+        a.columns = 16;
+        while (a.columns < a.tokens) a.columns *= 2;
+        a.stages = std::min(kFewStages, (kFewSmem - 1024) / few_stage_bytes(a.columns));
+        a.k_steps = static_cast<int32_t>(ceil_div(f.d_model, kStepK));
+        a.d_ff = f.d_ff;
+        a.h = h;
+        a.h_stride = h_stride;
+        a.save = saved;
+        a.act = f.act;
+        a.fault = d.fault;
+        e = encode(d, &a.x, m[0], kStepK, a.columns);
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = encode(d, &a.w[i], m[1 + i], kStepK, kFewRows);
+        if (e != cudaSuccess) return e;
+        few_kernel<<<static_cast<unsigned>(ceil_div(f.d_ff, kFewRows)), kFewThreads,
+                     1024 + a.stages * few_stage_bytes(a.columns), st>>>(a);
+        return cudaGetLastError();
+    }
     TileArgs a{};
     if ((e = dual_args(f, d, m, &a)) != cudaSuccess) return e;
     a.out[0] = h;

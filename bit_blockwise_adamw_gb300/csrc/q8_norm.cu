@@ -15,6 +15,8 @@
 // is written there) or is one of the two that reach over its ends.  norm_sum
 // adds up the CTAs' sums, in their order.
 #include <algorithm>
+#include <mutex>
+#include <set>
 
 #include "q8_internal.h"
 #include "q8_tc.cuh"
@@ -1110,10 +1112,16 @@ int sm_count()
 
 }  // namespace
 
+// Once for each device: kernels' shared-memory limits, launch configurations.
 cudaError_t prepare_norm()
 {
-    cudaError_t e = cudaSuccess;
-    int grid = 0;
+    static std::mutex lock;
+    static std::set<int> done;
+    int dev = 0, grid = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> guard(lock);
+    if (done.count(dev)) return cudaSuccess;
     for (bool f32 : {false, true})
         for (bool vec : {false, true})
             for (int64_t dim : {4096, 8192, 16384, 32768}) {
@@ -1129,6 +1137,7 @@ cudaError_t prepare_norm()
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
                 }
             }
+    if (e == cudaSuccess) done.insert(dev);
     return e;
 }
 
@@ -1173,8 +1182,7 @@ cudaError_t launch_norm_backward(const q8_block_norm& n, const q8_block_norm_gra
     a.fault = dev.fault;
     const bool layer = n.post_kind == Q8_NORM_LAYER || n.pre_kind == Q8_NORM_LAYER;
     const BackwardKernel k = p.staged ? staged_kernel(f32, layer, p.threads) : backward_kernel(f32, p.vec, layer, n.dim);
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
-    if (e != cudaSuccess) return e;
+    if ((e = prepare_norm()) != cudaSuccess) return e;
     k<<<static_cast<unsigned>(p.ctas), p.threads, static_cast<size_t>(p.smem), st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     SumArgs s{a.partial, a.gate_partial, {}, g.d_gate, p.ctas, n.dim, n.tokens, std::max<int64_t>(1, n.gate_tokens), 0};
