@@ -3,7 +3,8 @@
 The compute lives in libq8adamw.so (C ABI: include/q8adamw.h for the steps,
 include/q8train.h for the training-step operators around them); this package
 is its Python binding (same names as the C entry points) plus a torch.optim
-front end (bit_blockwise_adamw_gb300.optim).
+front end (bit_blockwise_adamw_gb300.optim) and autograd functions and modules
+(bit_blockwise_adamw_gb300.nn).
 """
 from ._binding import (  # noqa: F401
     BLOCK, DISTILL_MAX_K, EXPORTS, GELU, GELU_TANH, MAX_STEP, NORM_LAYER, NORM_MAX_DIM, NORM_NONE, NORM_RMS,
