@@ -5,8 +5,8 @@
 // pairs of CTAs (tile_kernel):
 //   kForward  [g | u] = x [w_gate | w_up]^T       epilogue: h = act(g) u
 //   kGates    the same product again              epilogue: dg, du from dh
-//   kInput    dx = dg w_gate + du w_up            one accumulation over 2 d_ff
-//   kWeight   dw_gate = dg^T x, dw_up = du^T x    two batches
+//   kProducts dx = dg w_gate + du w_up            one accumulation over 2 d_ff
+//             dw_gate = dg^T x, dw_up = du^T x    two batches, in the same launch
 // A pair owns a 256 x 256 tile of the result: each CTA holds 128 rows of A and
 // half of B's 256 rows, and the pair's tensor cores read both halves, so each
 // operand byte is fetched once for twice the products.  In kForward and kGates
@@ -14,7 +14,7 @@
 // rows, CTA 1 w_up's), so that one thread of the epilogue finds g and u of its
 // element in its own tensor-memory lane and no intermediate leaves the chip.
 // Operands stay as they lie in memory: an operand whose M or N index is
-// contiguous (weights in kInput, everything in kWeight) is loaded in boxes of
+// contiguous (the weights for dx, everything for dw) is loaded in boxes of
 // 64 of that index by 64 of K and given to the tensor core as MN-major.
 //
 // Roles: warp 0 loads (TMA, a ring of six 32 KB stages in each CTA), warp 1 of
@@ -22,6 +22,7 @@
 // tensor memory, whose 512 columns hold two accumulators, so that a tile's
 // epilogue runs under the next tile's products.
 #include <algorithm>
+#include <cmath>
 #include <map>
 #include <mutex>
 
@@ -46,19 +47,33 @@ constexpr int kTileThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kTileSmem = kStages * kStageBytes + 1024 + 256;
 constexpr int kRaster = 8;                                 // row tiles that share a sweep over the columns
 
-enum Mode { kForward, kGates, kInput, kWeight };
+constexpr int kMostPairs = 160;
 
-struct TileArgs {
+enum Mode { kForward, kGates, kProducts };
+enum { kInput, kWeight };                                  // the jobs of kProducts: dx, and the weights' gradients
+
+// One product: its tiles, by batch and by part of K.
+struct Job {
     CUtensorMap a[2], b[2];          // kForward, kGates: a[0]; b by CTA.  kInput: by segment.  kWeight: a by batch, b[0]
     int32_t m_tiles, n_tiles, batches, splits;
     int32_t k_steps, segments;       // stages of one segment, and segments
     int64_t M, N;                    // of one batch's result (N = d_ff where two accumulators share a tile)
     uint16_t* out[2];
     int64_t out_stride;
+    float* partial;                  // splits > 1: [batch, split, M, N]
+
+    __host__ __device__ int64_t units() const { return static_cast<int64_t>(batches) * splits * m_tiles * n_tiles; }
+};
+
+struct TileArgs {
+    Job job[2];                      // kForward, kGates: the first alone
+    // Pairs take every pairs-th unit of the first job; the last `late` of them,
+    // which have one unit less there, then take more of the second: all pairs take
+    // every pairs-th for `rounds` rounds, then the late ones alone the rest.
+    int32_t rounds, late;
     float* save;                     // kForward: g [M, N], then u, or NULL
     const uint16_t* dh;              // kGates
     int64_t dh_stride;
-    float* partial;                  // splits > 1: [batch, split, M, N]
     int32_t act;
     int32_t* fault;                  // host-mapped: set when a wait ran out
 };
@@ -67,12 +82,32 @@ struct TileArgs {
 // their results where these do not vanish.
 __device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
 
+// Phi(g) = erfc(-g / sqrt(2)) / 2, with erfc(z) = t exp(-z^2 + P(t)),
+// t = 1 / (1 + z / 2), z >= 0: the Chebyshev fit of Press et al., "Numerical
+// Recipes", 6.2, within 1.2e-7 of erfc relatively everywhere; no branches, where
+// erfcf's cost 5 us of 37 us of the forward product at 1023 tokens, 1600 x 6400.
+__device__ __forceinline__ float normal_cdf(float g)
+{
+    const float z = fabsf(g) * 0.70710678118654752f, t = __fdividef(1.0f, fmaf(0.5f, z, 1.0f));
+    float p = fmaf(t, 0.17087277f, -0.82215223f);
+    p = fmaf(t, p, 1.48851587f);
+    p = fmaf(t, p, -1.13520398f);
+    p = fmaf(t, p, 0.27886807f);
+    p = fmaf(t, p, -0.18628806f);
+    p = fmaf(t, p, 0.09678418f);
+    p = fmaf(t, p, 0.37409196f);
+    p = fmaf(t, p, 1.00002368f);
+    p = fmaf(t, p, -1.26551223f);
+    const float half = 0.5f * t * __expf(fmaf(-z, z, p));
+    return g < 0.0f ? half : 1.0f - half;
+}
+
 __device__ __forceinline__ float act_value(float g, int act)
 {
     if (act == Q8_SILU) return g * sigmoid(g);
     if (act == Q8_GELU_TANH)       // (1 + tanh t)/2 = sigmoid(2 t)
         return g * sigmoid(1.5957691216057308f * g * fmaf(0.044715f, g * g, 1.0f));
-    return 0.5f * g * erfcf(-0.70710678118654752f * g);
+    return g * normal_cdf(g);
 }
 
 __device__ __forceinline__ float2 act_both(float g, int act)
@@ -85,7 +120,7 @@ __device__ __forceinline__ float2 act_both(float g, int act)
         const float g2 = g * g, s = sigmoid(1.5957691216057308f * g * fmaf(0.044715f, g2, 1.0f));
         return make_float2(g * s, s + g * s * (1.0f - s) * 1.5957691216057308f * fmaf(0.134145f, g2, 1.0f));
     }
-    const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
+    const float cdf = normal_cdf(g);
     return make_float2(g * cdf, fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), cdf));
 }
 
@@ -156,7 +191,7 @@ struct Unit {
     int batch, split, m, n, k0, k1;
 };
 
-__device__ __forceinline__ Unit unit_of(const TileArgs& a, int i)
+__device__ __forceinline__ Unit unit_of(const Job& a, int i)
 {
     Unit u;
     const int tiles = a.m_tiles * a.n_tiles;
@@ -179,9 +214,7 @@ template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ TileArgs args)
 {
-    constexpr bool kAmn = MODE == kWeight, kBmn = MODE == kInput || MODE == kWeight;
-    constexpr bool kDual = MODE == kForward || MODE == kGates;
-    constexpr uint32_t kDesc = mma_desc(kAmn, kBmn, kPairM, kPairN);
+    constexpr bool kDual = MODE != kProducts;
 
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;      // 128-byte swizzle: 1024-byte aligned stages
@@ -196,7 +229,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int units = args.batches * args.splits * args.m_tiles * args.n_tiles;
+    // the pair's units, in the same order in every role; body returns false to stop
+    const auto for_units = [&](auto&& body) {
+        const int units = static_cast<int>(args.job[0].units());           // checked to fit
+        for (int i = pair; i < units; i += pairs)
+            if (!body(args.job[0], 0, i)) return;
+        if (kDual) return;
+        // from the last pair on, so that neighbours work on neighbouring tiles
+        const int second = static_cast<int>(args.job[1].units()), from = pairs - 1 - pair, common = args.rounds * pairs;
+        for (int i = from; i < min(second, common); i += pairs)
+            if (!body(args.job[1], 1, i)) return;
+        for (int i = common + from; from < args.late && i < second; i += args.late)
+            if (!body(args.job[1], 1, i)) return;
+    };
 
     if (warp == 0) {
         if (elect()) {
@@ -210,8 +255,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             }
             bar_init(done, 1);
             bar_init_fence();
-            tma_prefetch_map(&args.a[0]);
-            tma_prefetch_map(&args.b[0]);
+            tma_prefetch_map(&args.job[0].a[0]);
+            tma_prefetch_map(&args.job[0].b[0]);
         }
     } else if (warp == 1) {
         tmem_alloc_all(tmem_slot);
@@ -228,26 +273,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (elect()) {
             int s = 0;
             uint32_t phase = 1;                       // an empty stage's first wait passes
-            for (int i = pair; i < units && ok; i += pairs) {
-                const Unit u = unit_of(args, i);
+            for_units([&](const Job& job, int which, int i) {
+                const Unit u = unit_of(job, i);
+                const bool input = !kDual && which == kInput, weight = !kDual && which == kWeight;
                 const int m0 = u.m * kPairM + static_cast<int>(rank) * kHalf;
                 const int n0 = kDual ? u.n * kHalf : u.n * kPairN + static_cast<int>(rank) * kHalf;
                 for (int k = u.k0; k < u.k1; ++k) {
-                    if (!(ok = bar_wait(empty(s), phase))) break;
+                    if (!(ok = bar_wait(empty(s), phase))) return false;
                     if (rank == 0) bar_expect(full(s), 2 * kStageBytes);
                     const uint32_t bar = peer_addr(full(s), 0);
-                    const int seg = MODE == kInput ? k / args.k_steps : 0;
-                    const int x = (MODE == kInput ? k % args.k_steps : k) * kStepK;
-                    const CUtensorMap* a = &args.a[MODE == kWeight ? u.batch : seg];
-                    const CUtensorMap* b = &args.b[kDual ? rank : seg];
+                    const int seg = input ? k / job.k_steps : 0;
+                    const int x = (k - seg * job.k_steps) * kStepK;
+                    const CUtensorMap* a = &job.a[weight ? u.batch : seg];
+                    const CUtensorMap* b = &job.b[kDual ? rank : seg];
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kOperandBytes;
-                    if (kAmn) {
+                    if (weight) {
                         tma_load(sa, a, m0, x, bar);
                         tma_load(sa + kChunkBytes, a, m0 + 64, x, bar);
                     } else {
                         tma_load(sa, a, x, m0, bar);
                     }
-                    if (kBmn) {
+                    if (!kDual) {
                         tma_load(sb, b, n0, x, bar);
                         tma_load(sb + kChunkBytes, b, n0 + 64, x, bar);
                     } else {
@@ -255,7 +301,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                     }
                     if (++s == kStages) s = 0, phase ^= 1;
                 }
-            }
+                return true;
+            });
             // no load may be in flight when the CTA ends: every stage loaded
             // has been given back (the products over it have completed)
             for (int i = 0; i < kStages; ++i) {
@@ -267,29 +314,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (rank == 0 && elect()) {
             int s = 0, b = 0;
             uint32_t phase = 0, acc_phase = 1;
-            for (int i = pair; i < units && ok; i += pairs) {
-                const Unit u = unit_of(args, i);
-                if (!(ok = bar_wait<true>(acc_empty(b), acc_phase))) break;
+            for_units([&](const Job& job, int which, int i) {
+                const Unit u = unit_of(job, i);
+                // K-major: 8 rows of 128 bytes to a swizzle atom, K = 16 is 32 bytes on;
+                // MN-major: 8 of K by 64 of M to an atom, K = 16 is two atoms on
+                const bool a_mn = !kDual && which == kWeight;
+                const uint32_t desc = kDual ? mma_desc(false, false, kPairM, kPairN)
+                                            : a_mn ? mma_desc(true, true, kPairM, kPairN) : mma_desc(false, true, kPairM, kPairN);
+                const uint32_t a_step = a_mn ? 2048 : 32, a_lead = a_mn ? kChunkBytes : 16;
+                constexpr uint32_t b_step = kDual ? 32 : 2048, b_lead = kDual ? 16 : kChunkBytes;
+                if (!(ok = bar_wait<true>(acc_empty(b), acc_phase))) return false;
                 tc_fence_after();
                 const uint32_t d = tmem + b * kPairN;
                 for (int k = u.k0; k < u.k1; ++k) {
-                    if (!(ok = bar_wait(full(s), phase))) break;
+                    if (!(ok = bar_wait(full(s), phase))) return false;
                     tc_fence_after();
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kOperandBytes;
-                    // K-major: 8 rows of 128 bytes to a swizzle atom, K = 16 is 32 bytes on;
-                    // MN-major: 8 of K by 64 of M to an atom, K = 16 is two atoms on
 #pragma unroll
                     for (int j = 0; j < kStepK / 16; ++j)
-                        mma_pair(d, smem_desc(sa + j * (kAmn ? 2048 : 32), kAmn ? kChunkBytes : 16, 1024),
-                                 smem_desc(sb + j * (kBmn ? 2048 : 32), kBmn ? kChunkBytes : 16, 1024), kDesc,
+                        mma_pair(d, smem_desc(sa + j * a_step, a_lead, 1024), smem_desc(sb + j * b_step, b_lead, 1024), desc,
                                  k > u.k0 || j > 0);
                     mma_commit_pair(empty(s));
                     if (++s == kStages) s = 0, phase ^= 1;
                 }
-                if (!ok) break;
                 mma_commit_pair(acc_full(b));
                 if (++b == 2) b = 0, acc_phase ^= 1;
-            }
+                return true;
+            });
             mma_commit_pair(done);
             ok = bar_wait(done, 0) && ok;                // tensor memory is freed after this
         }
@@ -298,11 +349,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         int b = 0;
         uint32_t phase = 0;
-        for (int i = pair; i < units; i += pairs) {
-            const Unit u = unit_of(args, i);
+        for_units([&](const Job& job, int which, int i) {
+            const Unit u = unit_of(job, i);
             const int64_t m = static_cast<int64_t>(u.m) * kPairM + rank * kHalf + quad * 32 + lane;
-            const bool row = m < args.M;
-            if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(acc_full(b), phase)))) break;
+            const bool row = m < job.M;
+            if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(acc_full(b), phase)))) return false;
             tc_fence_after();
             const uint32_t t = lanes + b * kPairN;
             constexpr int kChunks = kDual ? 2 : 4;
@@ -311,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 float v[32], w[32];
                 const int col = (half * kChunks + c) * 32;
                 const int64_t n = static_cast<int64_t>(u.n) * (kDual ? kHalf : kPairN) + col;
-                const int64_t left = args.N - n;
+                const int64_t left = job.N - n;
                 tmem_load32(t + col, v);
                 if (kDual) tmem_load32(t + kHalf + col, w);
                 tmem_load_wait();
@@ -323,12 +374,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 if (!row || left <= 0) continue;
                 if (MODE == kForward) {
                     if (args.save) {
-                        store_row(args.save + m * args.N + n, v, left);
-                        store_row(args.save + (args.M + m) * args.N + n, w, left);
+                        store_row(args.save + m * job.N + n, v, left);
+                        store_row(args.save + (job.M + m) * job.N + n, w, left);
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], args.act) * w[j];
-                    store_row(args.out[0] + m * args.out_stride + n, v, left);
+                    store_row(job.out[0] + m * job.out_stride + n, v, left);
                 } else if (MODE == kGates) {
                     float d[32];
                     load_row(args.dh + m * args.dh_stride + n, d, left);
@@ -338,17 +389,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                         v[j] = d[j] * w[j] * a.y;
                         w[j] = d[j] * a.x;
                     }
-                    store_row(args.out[0] + m * args.out_stride + n, v, left);
-                    store_row(args.out[1] + m * args.out_stride + n, w, left);
-                } else if (args.splits > 1) {
-                    store_row(args.partial + ((static_cast<int64_t>(u.batch) * args.splits + u.split) * args.M + m) * args.N + n,
-                              v, left);
+                    store_row(job.out[0] + m * job.out_stride + n, v, left);
+                    store_row(job.out[1] + m * job.out_stride + n, w, left);
+                } else if (job.splits > 1) {
+                    store_row(job.partial + ((static_cast<int64_t>(u.batch) * job.splits + u.split) * job.M + m) * job.N + n, v,
+                              left);
                 } else {
-                    store_row(args.out[MODE == kWeight ? u.batch : 0] + m * args.out_stride + n, v, left);
+                    store_row(job.out[u.batch] + m * job.out_stride + n, v, left);
                 }
             }
             if (++b == 2) b = 0, phase ^= 1;
-        }
+            return true;
+        });
         // the second CTA's copy of the last arrival: it must land before the CTA ends
         if (rank == 1 && warp == 2) ok = bar_wait(done, 0) && ok;
     }
@@ -488,15 +540,45 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     if (warp == 1) tmem_free_single(tmem, tmem_columns);
 }
 
-// out = the sum of the splits' parts, in their order.
-__global__ void __launch_bounds__(256) join_kernel(const float* partial, int splits, int64_t M, int64_t N, uint16_t* out,
-                                                   int64_t out_stride)
+// out = the sum of the splits' parts, in their order: rows to blockIdx.x, four
+// columns to a thread, a result to blockIdx.y.
+struct Join {
+    const float* partial;
+    uint16_t* out;
+    int64_t M, N, out_stride;
+    int32_t splits;
+};
+struct JoinArgs {
+    Join join[3];
+};
+
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs args)
 {
-    const int64_t n = M * N;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        float s = partial[i];
-        for (int k = 1; k < splits; ++k) s += partial[k * n + i];
-        out[i / N * out_stride + i % N] = float_to_bf16(s);
+    const Join& a = args.join[blockIdx.y];
+    const int64_t part = a.M * a.N;
+    const bool whole = (a.N & 3) == 0 && (a.out_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const float* p = a.partial + m * a.N;
+        uint16_t* out = a.out + m * a.out_stride;
+        for (int64_t n = 4 * threadIdx.x; n < a.N; n += 4 * 256) {
+            if (whole) {
+                float4 s = *reinterpret_cast<const float4*>(p + n);
+                for (int k = 1; k < a.splits; ++k) {
+                    const float4 q = *reinterpret_cast<const float4*>(p + k * part + n);
+                    s.x += q.x;
+                    s.y += q.y;
+                    s.z += q.z;
+                    s.w += q.w;
+                }
+                *reinterpret_cast<uint2*>(out + n) = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
+            } else {
+                for (int64_t j = n; j < n + 4 && j < a.N; ++j) {
+                    float s = p[j];
+                    for (int k = 1; k < a.splits; ++k) s += p[k * part + j];
+                    out[j] = float_to_bf16(s);
+                }
+            }
+        }
     }
 }
 
@@ -551,13 +633,21 @@ __global__ void __launch_bounds__(256) gates_kernel(const float* save, const uin
     }
 }
 
-// A copy whose rows start on 16 bytes, for TMA.
+// A copy whose rows start on 16 bytes, for TMA: rows to blocks, eight columns to
+// a thread.
 __global__ void __launch_bounds__(256) align_kernel(const uint16_t* in, int64_t in_stride, int64_t rows, int64_t cols,
                                                     uint16_t* out, int64_t out_stride)
 {
-    const int64_t n = rows * cols;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
-        out[i / cols * out_stride + i % cols] = in[i / cols * in_stride + i % cols];
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const uint16_t* p = in + r * in_stride;
+        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * 256) {
+            uint32_t w[4] = {};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < cols) w[j / 2] |= static_cast<uint32_t>(p[c + j]) << (16 * (j & 1));
+            *reinterpret_cast<uint4*>(out + r * out_stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
 }
 
 // ------------------------------------------------------------------------- host
@@ -576,7 +666,7 @@ bool tma_ready(const void* p, int64_t stride) { return (reinterpret_cast<uintptr
 // The workspace: aligned copies of x and the weights where TMA cannot read
 // them in place, and for the backward call dg, du and the partial sums.
 struct Layout {
-    int64_t x = -1, w_gate = -1, w_up = -1, dg = -1, du = -1, partial = -1, bytes = 0;
+    int64_t x = -1, w_gate = -1, w_up = -1, dg = -1, du = -1, input = -1, weight = -1, bytes = 0;   // the last two: parts
     int64_t d_stride, f_stride;              // row strides of the copies, and of dg and du
 };
 
@@ -584,29 +674,29 @@ struct Device : DeviceInfo {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
-// How many parts K is cut into: with fewer tiles than pairs of SMs the idle
-// pairs take parts of K, at least eight stages each (what fills the ring).
-int splits_for(int64_t tiles, int64_t steps, int pairs)
-{
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(pairs / std::max<int64_t>(1, tiles), steps / 8)));
-}
-
+// The products of the backward call.  K is cut into parts where a tile alone
+// would take longer than the pairs' even share of all the work, at least eight
+// stages to a part (what fills the ring).
 struct Shape {
-    int64_t m_tiles, n_tiles, k_steps;
+    int64_t m_tiles, n_tiles, k_steps, segments;
     int splits;
 };
 
-Shape input_shape(const q8_gated_ff& f, int pairs)
-{
-    Shape s{ceil_div(f.tokens, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.d_ff, kStepK), 1};
-    s.splits = splits_for(s.m_tiles * s.n_tiles, 2 * s.k_steps, pairs);
-    return s;
-}
+struct Shapes {
+    Shape input, weight;
+};
 
-Shape weight_shape(const q8_gated_ff& f, int pairs)
+Shapes shapes_of(const q8_gated_ff& f, int pairs)
 {
-    Shape s{ceil_div(f.d_ff, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.tokens, kStepK), 1};
-    s.splits = splits_for(2 * s.m_tiles * s.n_tiles, s.k_steps, pairs);
+    Shapes s{{ceil_div(f.tokens, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.d_ff, kStepK), 2, 1},
+             {ceil_div(f.d_ff, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.tokens, kStepK), 1, 1}};
+    const double all = static_cast<double>(s.input.m_tiles) * s.input.n_tiles * 2 * s.input.k_steps +
+                       2.0 * s.weight.m_tiles * s.weight.n_tiles * s.weight.k_steps;
+    const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(all / pairs));
+    for (Shape* j : {&s.input, &s.weight}) {
+        const int64_t steps = j->k_steps * j->segments;
+        j->splits = static_cast<int>(std::max<int64_t>(1, std::min(ceil_div(steps, share), steps / 8)));
+    }
     return s;
 }
 
@@ -629,7 +719,7 @@ cudaError_t device(Device* out)
         if ((e = device_info(&d)) != cudaSuccess) return e;
         const void* kernels[] = {
             reinterpret_cast<const void*>(tile_kernel<kForward>), reinterpret_cast<const void*>(tile_kernel<kGates>),
-            reinterpret_cast<const void*>(tile_kernel<kInput>), reinterpret_cast<const void*>(tile_kernel<kWeight>)};
+            reinterpret_cast<const void*>(tile_kernel<kProducts>)};
         for (const void* k : kernels)
             if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem)) != cudaSuccess) return e;
         if ((e = cudaFuncSetAttribute(few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem)) != cudaSuccess) return e;
@@ -639,7 +729,8 @@ cudaError_t device(Device* out)
     return cudaSuccess;
 }
 
-int pairs_of(const Device& d) { return std::max(1, d.sms / 2); }
+int pairs_of(int sms) { return std::max(1, std::min(sms / 2, kMostPairs)); }
+int pairs_of(const Device& d) { return pairs_of(d.sms); }
 
 // Two-dimensional map of m, boxes of box_cols x box_rows with the 128-byte
 // swizzle; what lies outside reads as zeros.
@@ -672,10 +763,9 @@ Layout layout(const q8_gated_ff& f, bool backward, int pairs)
     if (backward) {
         l.dg = take(f.tokens * l.f_stride * 2);
         l.du = take(f.tokens * l.f_stride * 2);
-        const Shape i = input_shape(f, pairs), w = weight_shape(f, pairs);
-        const int64_t need = std::max(i.splits > 1 ? i.splits * f.tokens * f.d_model : 0,
-                                      w.splits > 1 ? 2 * w.splits * f.d_ff * f.d_model : 0);
-        if (need) l.partial = take(need * 4);
+        const Shapes s = shapes_of(f, pairs);
+        if (s.input.splits > 1) l.input = take(s.input.splits * f.tokens * f.d_model * 4);
+        if (s.weight.splits > 1) l.weight = take(2 * s.weight.splits * f.d_ff * f.d_model * 4);
     }
     return l;
 }
@@ -684,6 +774,8 @@ unsigned blocks_for(int64_t n, const Device& d)
 {
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 256), d.sms * int64_t(8))));
 }
+
+unsigned rows_for(int64_t rows, const Device& d) { return static_cast<unsigned>(std::min<int64_t>(rows, d.sms * int64_t(16))); }
 
 // x and the weights as TMA may read them.
 cudaError_t operands(const q8_gated_ff& f, const Layout& l, const Device& d, cudaStream_t st, Matrix m[3])
@@ -695,7 +787,7 @@ cudaError_t operands(const q8_gated_ff& f, const Layout& l, const Device& d, cud
     for (int i = 0; i < 3; ++i) {
         if (at[i] < 0) continue;
         uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(f.workspace) + at[i]);
-        align_kernel<<<blocks_for(m[i].rows * m[i].cols, d), 256, 0, st>>>(m[i].p, m[i].stride, m[i].rows, m[i].cols, copy,
+        align_kernel<<<rows_for(m[i].rows, d), 256, 0, st>>>(m[i].p, m[i].stride, m[i].rows, m[i].cols, copy,
                                                                           l.d_stride);
         m[i].p = copy;
         m[i].stride = l.d_stride;
@@ -704,29 +796,57 @@ cudaError_t operands(const q8_gated_ff& f, const Layout& l, const Device& d, cud
 }
 
 template <int MODE>
-cudaError_t run_tiles(const TileArgs& a, const Device& d, cudaStream_t st)
+cudaError_t run_tiles(TileArgs& a, const Device& d, cudaStream_t st)
 {
-    const int64_t units = static_cast<int64_t>(a.batches) * a.splits * a.m_tiles * a.n_tiles;
-    if (units >= (int64_t(1) << 31) - 2 * pairs_of(d)) return cudaErrorInvalidValue;
-    tile_kernel<MODE><<<static_cast<unsigned>(2 * std::min<int64_t>(units, pairs_of(d))), kTileThreads, kTileSmem, st>>>(a);
+    const int pairs = pairs_of(d);
+    int64_t units[2];
+    for (int i = 0; i < 2; ++i) {
+        units[i] = a.job[i].units();
+        if (units[i] >= (int64_t(1) << 31) - 2 * pairs) return cudaErrorInvalidValue;
+    }
+    // the second job's units go to the pairs so that all have about the same
+    // number of steps, counting those of the first job
+    const auto steps = [&](int i) { return units[i] ? static_cast<double>(a.job[i].k_steps) * a.job[i].segments / a.job[i].splits : 0.0; };
+    const int64_t ahead = units[0] % pairs;                  // pairs that have one more unit of the first job
+    a.late = static_cast<int32_t>(pairs - ahead);
+    if (units[1]) {
+        const double share = (units[0] * steps(0) + units[1] * steps(1)) / pairs;
+        const double left = share - (units[0] / pairs + (ahead > 0)) * steps(0);
+        a.rounds = static_cast<int32_t>(std::min<double>(std::floor(std::max(0.0, left) / steps(1) + 0.5), static_cast<double>(units[1])));
+        if (static_cast<int64_t>(a.rounds) * pairs > units[1]) a.rounds = static_cast<int32_t>(ceil_div(units[1], pairs));
+    }
+    const int64_t grid = units[1] ? pairs : std::min<int64_t>(units[0], pairs);
+    a.fault = d.fault;
+    tile_kernel<MODE><<<static_cast<unsigned>(2 * grid), kTileThreads, kTileSmem, st>>>(a);
     return cudaGetLastError();
 }
 
 // Where the product of x with both weights goes: kForward and kGates.
 cudaError_t dual_args(const q8_gated_ff& f, const Device& d, const Matrix m[3], TileArgs* a)
 {
-    a->m_tiles = static_cast<int32_t>(ceil_div(f.tokens, kPairM));
-    a->n_tiles = static_cast<int32_t>(ceil_div(f.d_ff, kHalf));
-    a->batches = a->splits = a->segments = 1;
-    a->k_steps = static_cast<int32_t>(ceil_div(f.d_model, kStepK));
-    a->M = f.tokens;
-    a->N = f.d_ff;
+    Job& j = a->job[0];
+    j.m_tiles = static_cast<int32_t>(ceil_div(f.tokens, kPairM));
+    j.n_tiles = static_cast<int32_t>(ceil_div(f.d_ff, kHalf));
+    j.batches = j.splits = j.segments = 1;
+    j.k_steps = static_cast<int32_t>(ceil_div(f.d_model, kStepK));
+    j.M = f.tokens;
+    j.N = f.d_ff;
     a->act = f.act;
-    a->fault = d.fault;
-    cudaError_t e = encode(d, &a->a[0], m[0], kStepK, kHalf);
-    if (e == cudaSuccess) e = encode(d, &a->b[0], m[1], kStepK, kHalf);
-    if (e == cudaSuccess) e = encode(d, &a->b[1], m[2], kStepK, kHalf);
+    cudaError_t e = encode(d, &j.a[0], m[0], kStepK, kHalf);
+    if (e == cudaSuccess) e = encode(d, &j.b[0], m[1], kStepK, kHalf);
+    if (e == cudaSuccess) e = encode(d, &j.b[1], m[2], kStepK, kHalf);
     return e;
+}
+
+void set_shape(Job* j, const Shape& s, int64_t M, int64_t N)
+{
+    j->m_tiles = static_cast<int32_t>(s.m_tiles);
+    j->n_tiles = static_cast<int32_t>(s.n_tiles);
+    j->splits = s.splits;
+    j->k_steps = static_cast<int32_t>(s.k_steps);
+    j->segments = static_cast<int32_t>(s.segments);
+    j->M = M;
+    j->N = N;
 }
 
 }  // namespace
@@ -744,7 +864,7 @@ int64_t ff_workspace(const q8_gated_ff& f, bool backward)
         cudaGetLastError();
         sms = 152;
     }
-    return layout(f, backward, std::max(1, sms / 2)).bytes;
+    return layout(f, backward, pairs_of(sms)).bytes;
 }
 
 cudaError_t launch_ff_forward(const q8_gated_ff& f, uint16_t* h, int64_t h_stride, float* saved, cudaStream_t st)
@@ -778,8 +898,8 @@ cudaError_t launch_ff_forward(const q8_gated_ff& f, uint16_t* h, int64_t h_strid
     }
     TileArgs a{};
     if ((e = dual_args(f, d, m, &a)) != cudaSuccess) return e;
-    a.out[0] = h;
-    a.out_stride = h_stride;
+    a.job[0].out[0] = h;
+    a.job[0].out_stride = h_stride;
     a.save = saved;
     return run_tiles<kForward>(a, d, st);
 }
@@ -793,7 +913,6 @@ cudaError_t launch_ff_backward(const q8_gated_ff& f, const FfBackward& b, cudaSt
     const Layout l = layout(f, true, pairs_of(d));
     uint8_t* ws = static_cast<uint8_t*>(f.workspace);
     uint16_t *dg = reinterpret_cast<uint16_t*>(ws + l.dg), *du = reinterpret_cast<uint16_t*>(ws + l.du);
-    float* partial = l.partial < 0 ? nullptr : reinterpret_cast<float*>(ws + l.partial);
     Matrix m[3];
     if ((e = operands(f, l, d, st, m)) != cudaSuccess) return e;
     if (b.saved) {
@@ -803,66 +922,67 @@ cudaError_t launch_ff_backward(const q8_gated_ff& f, const FfBackward& b, cudaSt
     } else {
         TileArgs a{};
         if ((e = dual_args(f, d, m, &a)) != cudaSuccess) return e;
-        a.out[0] = dg;
-        a.out[1] = du;
-        a.out_stride = l.f_stride;
+        a.job[0].out[0] = dg;
+        a.job[0].out[1] = du;
+        a.job[0].out_stride = l.f_stride;
         a.dh = b.dh;
         a.dh_stride = b.dh_stride;
         if ((e = run_tiles<kGates>(a, d, st)) != cudaSuccess) return e;
     }
-    const Matrix g{dg, f.tokens, f.d_ff, l.f_stride}, u{du, f.tokens, f.d_ff, l.f_stride};
-    auto join = [&](const TileArgs& a, int batch) {
-        join_kernel<<<blocks_for(a.M * a.N, d), 256, 0, st>>>(a.partial + static_cast<int64_t>(batch) * a.splits * a.M * a.N,
-                                                              a.splits, a.M, a.N, a.out[batch], a.out_stride);
-        return cudaGetLastError();
-    };
+    const Matrix grad[2] = {{dg, f.tokens, f.d_ff, l.f_stride}, {du, f.tokens, f.d_ff, l.f_stride}};
+    const Shapes s = shapes_of(f, pairs_of(d));
+    TileArgs a{};
     if (b.dx) {
-        const Shape s = input_shape(f, pairs_of(d));
-        TileArgs a{};
-        a.m_tiles = static_cast<int32_t>(s.m_tiles);
-        a.n_tiles = static_cast<int32_t>(s.n_tiles);
-        a.batches = 1;
-        a.splits = s.splits;
-        a.k_steps = static_cast<int32_t>(s.k_steps);
-        a.segments = 2;
-        a.M = f.tokens;
-        a.N = f.d_model;
-        a.out[0] = b.dx;
-        a.out_stride = b.dx_stride;
-        a.partial = partial;
-        a.fault = d.fault;
-        const Matrix da[2] = {g, u};
+        Job& j = a.job[kInput];
+        set_shape(&j, s.input, f.tokens, f.d_model);
+        j.batches = 1;
+        j.out[0] = b.dx;
+        j.out_stride = b.dx_stride;
+        j.partial = reinterpret_cast<float*>(ws + l.input);
         for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-            e = encode(d, &a.a[i], da[i], kStepK, kHalf);
-            if (e == cudaSuccess) e = encode(d, &a.b[i], m[1 + i], 64, kStepK);
+            e = encode(d, &j.a[i], grad[i], kStepK, kHalf);
+            if (e == cudaSuccess) e = encode(d, &j.b[i], m[1 + i], 64, kStepK);
         }
-        if (e == cudaSuccess) e = run_tiles<kInput>(a, d, st);
-        if (e == cudaSuccess && a.splits > 1) e = join(a, 0);
-        if (e != cudaSuccess) return e;
     }
-    if (b.dw_gate || b.dw_up) {
-        const Shape s = weight_shape(f, pairs_of(d));
-        TileArgs a{};
-        a.m_tiles = static_cast<int32_t>(s.m_tiles);
-        a.n_tiles = static_cast<int32_t>(s.n_tiles);
-        a.splits = s.splits;
-        a.k_steps = static_cast<int32_t>(s.k_steps);
-        a.segments = 1;
-        a.M = f.d_ff;
-        a.N = f.d_model;
-        a.out_stride = f.d_model;
-        a.partial = partial;
-        a.fault = d.fault;
-        const Matrix da[2] = {g, u};
-        uint16_t* dw[2] = {b.dw_gate, b.dw_up};
+    uint16_t* dw[2] = {b.dw_gate, b.dw_up};
+    if (dw[0] || dw[1]) {
+        Job& j = a.job[kWeight];
+        set_shape(&j, s.weight, f.d_ff, f.d_model);
+        j.out_stride = f.d_model;
+        j.partial = reinterpret_cast<float*>(ws + l.weight);
         for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
             if (!dw[i]) continue;
-            a.out[a.batches] = dw[i];
-            e = encode(d, &a.a[a.batches++], da[i], 64, kStepK);
+            j.out[j.batches] = dw[i];
+            e = encode(d, &j.a[j.batches++], grad[i], 64, kStepK);
         }
-        if (e == cudaSuccess) e = encode(d, &a.b[0], m[0], 64, kStepK);
-        if (e == cudaSuccess) e = run_tiles<kWeight>(a, d, st);
-        for (int i = 0; i < a.batches && e == cudaSuccess && a.splits > 1; ++i) e = join(a, i);
+        if (e == cudaSuccess) e = encode(d, &j.b[0], m[0], 64, kStepK);
+    }
+    // Both jobs in one launch fill the last rounds of one with the other's tiles
+    // (1023 tokens, 1600 x 6400, backward with forward: 141 us apart, 127 us
+    // together); with many rounds there is little to fill, and tiles of two jobs
+    // at a time share less of L2 (8192 tokens, 4096 x 16384: 1 % slower together).
+    const int64_t units = a.job[0].units() + a.job[1].units();
+    if (units <= 16 * pairs_of(d)) {
+        if (e == cudaSuccess) e = run_tiles<kProducts>(a, d, st);
+    } else {
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+            TileArgs one = a;
+            one.job[1 - i].batches = 0;
+            if (one.job[i].batches) e = run_tiles<kProducts>(one, d, st);
+        }
+    }
+    JoinArgs joins{};
+    unsigned count = 0;
+    int64_t rows = 0;
+    for (const Job& j : a.job)
+        for (int i = 0; i < j.batches && j.splits > 1; ++i) {
+            joins.join[count++] = Join{j.partial + static_cast<int64_t>(i) * j.splits * j.M * j.N, j.out[i], j.M, j.N, j.out_stride,
+                                       j.splits};
+            rows = std::max(rows, j.M);
+        }
+    if (e == cudaSuccess && count) {
+        join_kernel<<<dim3(rows_for(rows, d), count), 256, 0, st>>>(joins);
+        e = cudaGetLastError();
     }
     return e;
 }
