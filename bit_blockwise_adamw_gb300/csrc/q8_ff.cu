@@ -44,7 +44,7 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kChunkBytes = 64 * kStepK * 2;               // 64 of M or N by 64 of K
 constexpr int kEpilogueWarps = 8;
 constexpr int kTileThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kTileSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kTileSmem = kStages * kStageBytes + 1024 + 256 + kEpilogueWarps * 32 * 17 * 4;
 constexpr int kRaster = 8;                                 // row tiles that share a sweep over the columns
 
 constexpr int kMostPairs = 160;
@@ -136,34 +136,68 @@ __device__ __forceinline__ void store32(void* p, const uint32_t r[8])
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 
-// 32 consecutive elements of a row, `left` of which exist: in 32-byte stores
-// where they are whole and aligned, element by element at an edge.
-__device__ __forceinline__ void store_row(uint16_t* p, const float v[32], int64_t left)
+__device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    if (left >= 32 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+
+// 32 consecutive elements of a row on 16 bytes.
+__device__ __forceinline__ void store_row(uint16_t* p, const float v[32])
+{
+    uint32_t r[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t r[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = pack2(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
-            store32(p + 16 * i, r);
-        }
+    for (int j = 0; j < 16; ++j) r[j] = pack2(v[2 * j], v[2 * j + 1]);
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        store32(p, r);
+        store32(p + 16, r + 8);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left) p[i] = float_to_bf16(v[i]);
+        for (int j = 0; j < 16; j += 4) store16(p + 2 * j, r[j], r[j + 1], r[j + 2], r[j + 3]);
     }
 }
 
-__device__ __forceinline__ void store_row(float* p, const float v[32], int64_t left)
+__device__ __forceinline__ void store_row(float* p, const float v[32])
 {
-    if (left >= 32 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store32(p + 8 * i, reinterpret_cast<const uint32_t*>(v + 8 * i));
+        for (int j = 0; j < 32; j += 8) store32(p + j, r + j);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left) p[i] = v[i];
+        for (int j = 0; j < 32; j += 4) store16(p + j, r[j], r[j + 1], r[j + 2], r[j + 3]);
+    }
+}
+
+// A warp's 32 x 32 elements (a row to a lane) to rows `stride` apart, of which
+// `rows` and of whose columns `cols` exist.  Rows on 16 bytes are stored lane by
+// lane; others, and a matrix's last columns, go through the warp's shared memory
+// so that a store still covers consecutive addresses (2968 tokens, 927 x 8576:
+// element by element from the lanes the two backward products took 318 us).
+constexpr int kTurnWords = 32 * 17;
+
+template <typename T>
+__device__ __forceinline__ void store_block(T* p, int64_t stride, int64_t rows, int64_t cols, const float v[32], float* turn, int lane)
+{
+    if (cols >= 32 && ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride * sizeof(T))) & 15) == 0) {
+        if (lane < rows) store_row(p + lane * stride, v);
+        return;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) turn[lane * 17 + j] = v[16 * half + j];
+        __syncwarp();
+        const int col = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int row = 2 * i + (lane >> 4);
+            if (row < rows && 16 * half + col < cols) {
+                const float x = turn[row * 17 + col];
+                if constexpr (sizeof(T) == 2) p[row * stride + 16 * half + col] = float_to_bf16(x);
+                else p[row * stride + 16 * half + col] = x;
+            }
+        }
     }
 }
 
@@ -347,12 +381,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     } else {
         const int quad = warp & 3, half = (warp - 2) >> 2;       // 32 lanes, and half of the columns
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        float* turn = reinterpret_cast<float*>(raw + (bars + 256 - smem_addr(raw))) + (warp - 2) * kTurnWords;
         int b = 0;
         uint32_t phase = 0;
         for_units([&](const Job& job, int which, int i) {
             const Unit u = unit_of(job, i);
-            const int64_t m = static_cast<int64_t>(u.m) * kPairM + rank * kHalf + quad * 32 + lane;
-            const bool row = m < job.M;
+            const int64_t m = static_cast<int64_t>(u.m) * kPairM + rank * kHalf + quad * 32, rows = job.M - m;
             if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(acc_full(b), phase)))) return false;
             tc_fence_after();
             const uint32_t t = lanes + b * kPairN;
@@ -371,31 +405,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive_cluster(peer_addr(acc_empty(b), 0));
                 }
-                if (!row || left <= 0) continue;
+                if (rows <= 0 || left <= 0) continue;    // for all of the warp
                 if (MODE == kForward) {
                     if (args.save) {
-                        store_row(args.save + m * job.N + n, v, left);
-                        store_row(args.save + (job.M + m) * job.N + n, w, left);
+                        store_block(args.save + m * job.N + n, job.N, rows, left, v, turn, lane);
+                        store_block(args.save + (job.M + m) * job.N + n, job.N, rows, left, w, turn, lane);
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], args.act) * w[j];
-                    store_row(job.out[0] + m * job.out_stride + n, v, left);
+                    store_block(job.out[0] + m * job.out_stride + n, job.out_stride, rows, left, v, turn, lane);
                 } else if (MODE == kGates) {
                     float d[32];
-                    load_row(args.dh + m * args.dh_stride + n, d, left);
+                    load_row(args.dh + (m + lane) * args.dh_stride + n, d, lane < rows ? left : 0);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const float2 a = act_both(v[j], args.act);
                         v[j] = d[j] * w[j] * a.y;
                         w[j] = d[j] * a.x;
                     }
-                    store_row(job.out[0] + m * job.out_stride + n, v, left);
-                    store_row(job.out[1] + m * job.out_stride + n, w, left);
+                    store_block(job.out[0] + m * job.out_stride + n, job.out_stride, rows, left, v, turn, lane);
+                    store_block(job.out[1] + m * job.out_stride + n, job.out_stride, rows, left, w, turn, lane);
                 } else if (job.splits > 1) {
-                    store_row(job.partial + ((static_cast<int64_t>(u.batch) * job.splits + u.split) * job.M + m) * job.N + n, v,
-                              left);
+                    store_block(job.partial + ((static_cast<int64_t>(u.batch) * job.splits + u.split) * job.M + m) * job.N + n, job.N,
+                                rows, left, v, turn, lane);
                 } else {
-                    store_row(job.out[u.batch] + m * job.out_stride + n, v, left);
+                    store_block(job.out[u.batch] + m * job.out_stride + n, job.out_stride, rows, left, v, turn, lane);
                 }
             }
             if (++b == 2) b = 0, phase ^= 1;
@@ -417,13 +451,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 // are the tensor core's M then (64 rows of w_gate over the same 64 of w_up: one
 // 128-row tile), the tokens its N, padded to 16, 32, 64 or 128 instead of 256;
 // a CTA has a tile, and two CTAs on an SM keep 200 KB of weights in flight.
-// A lane of tensor memory is a column of h: lanes 64..127 pass u through shared
-// memory to lanes 0..63.
+// Where tiles are fewer than half the SMs a cluster of 2, 4 or 8 CTAs shares a
+// tile's K and the first adds up the others' parts, which they write to its
+// shared memory (78 tokens, 2752 x 601, 10 tiles: 29 us alone, SPLIT us with
+// eight; with as many tiles as SMs parts only take the loads of a row apart:
+// 24 tokens, 2560 x 10240: 36 us with two).
+// A lane of tensor memory is a column of g (0..63) or u (64..127): they meet
+// through shared memory.
 constexpr int kFewTokens = 128, kFewRows = 64, kFewThreads = 128, kFewStages = 8;
 
 struct FewArgs {
     CUtensorMap x, w[2];
     int32_t tokens, columns, stages, k_steps;        // columns: the padded tokens
+    int32_t parts;                   // CTAs to a tile
     int64_t d_ff;
     uint16_t* h;
     int64_t h_stride;
@@ -447,7 +487,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     const auto empty = [&](int s) { return smem_addr(&s_bar[kFewStages + s]); };
     const uint32_t done = smem_addr(&s_bar[2 * kFewStages]);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int f0 = blockIdx.x * kFewRows;
+    const int part = static_cast<int>(cluster_rank());
+    const int f0 = blockIdx.x / args.parts * kFewRows;
+    const int k0 = args.k_steps * part / args.parts, k1 = args.k_steps * (part + 1) / args.parts;
     const uint32_t tmem_columns = max(32, args.columns);
 
     if (warp == 0 && elect()) {
@@ -468,7 +510,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     if (warp == 0 && elect()) {
         int s = 0;
         uint32_t phase = 1;
-        for (int k = 0; k < args.k_steps; ++k) {
+        for (int k = k0; k < k1; ++k) {
             if (!(ok = bar_wait(empty(s), phase))) break;
             bar_expect(full(s), stage_bytes);
             const uint32_t sa = base + s * stage_bytes;
@@ -486,13 +528,13 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         const uint32_t desc = mma_desc(false, false, 128, args.columns);
         int s = 0;
         uint32_t phase = 0;
-        for (int k = 0; k < args.k_steps; ++k) {
+        for (int k = k0; k < k1; ++k) {
             if (!(ok = bar_wait(full(s), phase))) break;
             tc_fence_after();
             const uint32_t sa = base + s * stage_bytes, sb = sa + kOperandBytes;
 #pragma unroll
             for (int j = 0; j < kStepK / 16; ++j)
-                mma_single(tmem, smem_desc(sa + j * 32, 16, 1024), smem_desc(sb + j * 32, 16, 1024), desc, k > 0 || j > 0);
+                mma_single(tmem, smem_desc(sa + j * 32, 16, 1024), smem_desc(sb + j * 32, 16, 1024), desc, k > k0 || j > 0);
             mma_commit_single(empty(s));
             if (++s == args.stages) s = 0, phase ^= 1;
         }
@@ -506,33 +548,55 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     const int l = (warp & 1) * 32 + lane;
     const int64_t f = static_cast<int64_t>(f0) + l;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    float* s_u = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));      // [columns][64], over the stages
-    __syncthreads();                                 // which nobody reads any more
+    // over the stages, which nobody reads any more: the other CTAs' parts
+    // [parts - 1][columns][128], then what the warps of g and those of u give one
+    // another, [columns][64]
+    float* s_part = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
+    float* s_other = s_part + (args.parts - 1) * args.columns * 128;
     float v[16];
-    if (warp >= 2) {
-        for (int c = 0; c < args.columns; c += 16) {
-            tmem_load16(lanes + c, v);
-            tmem_load_wait();
+    if (args.parts > 1) {
+        cluster_sync();                              // all have read their stages
+        if (part > 0) {
+            const uint32_t to = peer_addr(smem_addr(s_part + (part - 1) * args.columns * 128 + warp * 32 + lane), 0);
+            for (int c = 0; c < args.columns; c += 16) {
+                tmem_load16(lanes + c, v);
+                tmem_load_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                s_u[(c + j) * kFewRows + l] = v[j];
-                if (args.save && c + j < args.tokens && f < args.d_ff)
-                    args.save[(static_cast<int64_t>(args.tokens) + c + j) * args.d_ff + f] = v[j];
+                for (int j = 0; j < 16; ++j)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (c + j) * 512), "f"(v[j]) : "memory");
             }
         }
+        cluster_sync();
+    } else {
+        __syncthreads();
     }
-    __syncthreads();
-    if (warp < 2) {
+    const auto column = [&](int c) {
+        tmem_load16(lanes + c, v);
+        tmem_load_wait();
+        for (int p = 0; p < args.parts - 1; ++p)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += s_part[(p * args.columns + c + j) * 128 + warp * 32 + lane];
+    };
+    // the warps of g (0, 1) make h for the first half of the tokens, those of u for
+    // the second; each gives the other its values of the other's half first
+    const int side = warp >> 1;
+    const auto own = [&](int c) { return (2 * c >= args.columns) == (side == 1); };
+    for (int pass = 0; pass < 2 && part == 0; ++pass) {
         for (int c = 0; c < args.columns; c += 16) {
-            tmem_load16(lanes + c, v);
-            tmem_load_wait();
+            if (own(c) != (pass == 1)) continue;
+            column(c);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                if (c + j >= args.tokens || f >= args.d_ff) continue;
-                if (args.save) args.save[static_cast<int64_t>(c + j) * args.d_ff + f] = v[j];
-                args.h[(c + j) * args.h_stride + f] = float_to_bf16(act_value(v[j], args.act) * s_u[(c + j) * kFewRows + l]);
+                const bool in = c + j < args.tokens && f < args.d_ff;
+                if (in && args.save) args.save[(static_cast<int64_t>(side) * args.tokens + c + j) * args.d_ff + f] = v[j];
+                float* other = s_other + (c + j) * kFewRows + l;
+                if (pass == 0) *other = v[j];
+                else if (in)
+                    args.h[(c + j) * args.h_stride + f] =
+                        float_to_bf16(side ? act_value(*other, args.act) * v[j] : act_value(v[j], args.act) * *other);
             }
         }
+        __syncthreads();
     }
     if (!ok) atomicExch_system(args.fault, 1);
     tc_fence_before();
@@ -633,19 +697,29 @@ __global__ void __launch_bounds__(256) gates_kernel(const float* save, const uin
     }
 }
 
-// A copy whose rows start on 16 bytes, for TMA: rows to blocks, eight columns to
-// a thread.
-__global__ void __launch_bounds__(256) align_kernel(const uint16_t* in, int64_t in_stride, int64_t rows, int64_t cols,
-                                                    uint16_t* out, int64_t out_stride)
+// Copies whose rows start on 16 bytes, for TMA: rows to blocks, eight columns to
+// a thread, a matrix to blockIdx.y.
+struct Align {
+    const uint16_t* in;
+    uint16_t* out;
+    int64_t rows, in_stride;
+};
+struct AlignArgs {
+    Align align[3];
+    int64_t cols, out_stride;
+};
+
+__global__ void __launch_bounds__(256) align_kernel(const __grid_constant__ AlignArgs args)
 {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const uint16_t* p = in + r * in_stride;
-        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * 256) {
+    const Align& a = args.align[blockIdx.y];
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const uint16_t* p = a.in + r * a.in_stride;
+        for (int64_t c = 8 * threadIdx.x; c < args.cols; c += 8 * 256) {
             uint32_t w[4] = {};
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (c + j < cols) w[j / 2] |= static_cast<uint32_t>(p[c + j]) << (16 * (j & 1));
-            *reinterpret_cast<uint4*>(out + r * out_stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (c + j < args.cols) w[j / 2] |= static_cast<uint32_t>(p[c + j]) << (16 * (j & 1));
+            *reinterpret_cast<uint4*>(a.out + r * args.out_stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
@@ -674,6 +748,11 @@ struct Device : DeviceInfo {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
+// What a unit of n stages costs a pair, in stages: reading a tile out of tensor
+// memory and storing it takes as long as some six stages, under the next tile's
+// products where these are longer.
+double cost_of(double n) { return n + 6.0; }
+
 // The products of the backward call.  K is cut into parts where a tile alone
 // would take longer than the pairs' even share of all the work, at least eight
 // stages to a part (what fills the ring).
@@ -690,8 +769,8 @@ Shapes shapes_of(const q8_gated_ff& f, int pairs)
 {
     Shapes s{{ceil_div(f.tokens, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.d_ff, kStepK), 2, 1},
              {ceil_div(f.d_ff, kPairM), ceil_div(f.d_model, kPairN), ceil_div(f.tokens, kStepK), 1, 1}};
-    const double all = static_cast<double>(s.input.m_tiles) * s.input.n_tiles * 2 * s.input.k_steps +
-                       2.0 * s.weight.m_tiles * s.weight.n_tiles * s.weight.k_steps;
+    const double all = static_cast<double>(s.input.m_tiles) * s.input.n_tiles * cost_of(2.0 * s.input.k_steps) +
+                       2.0 * s.weight.m_tiles * s.weight.n_tiles * cost_of(static_cast<double>(s.weight.k_steps));
     const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(all / pairs));
     for (Shape* j : {&s.input, &s.weight}) {
         const int64_t steps = j->k_steps * j->segments;
@@ -784,14 +863,20 @@ cudaError_t operands(const q8_gated_ff& f, const Layout& l, const Device& d, cud
     m[1] = Matrix{f.w_gate, f.d_ff, f.d_model, f.d_model};
     m[2] = Matrix{f.w_up, f.d_ff, f.d_model, f.d_model};
     const int64_t at[3] = {l.x, l.w_gate, l.w_up};
+    AlignArgs a{};
+    a.cols = f.d_model;
+    a.out_stride = l.d_stride;
+    unsigned count = 0;
+    int64_t rows = 0;
     for (int i = 0; i < 3; ++i) {
         if (at[i] < 0) continue;
         uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(f.workspace) + at[i]);
-        align_kernel<<<rows_for(m[i].rows, d), 256, 0, st>>>(m[i].p, m[i].stride, m[i].rows, m[i].cols, copy,
-                                                                          l.d_stride);
+        a.align[count++] = Align{m[i].p, copy, m[i].rows, m[i].stride};
+        rows = std::max(rows, m[i].rows);
         m[i].p = copy;
         m[i].stride = l.d_stride;
     }
+    if (count) align_kernel<<<dim3(rows_for(rows, d), count), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -805,8 +890,11 @@ cudaError_t run_tiles(TileArgs& a, const Device& d, cudaStream_t st)
         if (units[i] >= (int64_t(1) << 31) - 2 * pairs) return cudaErrorInvalidValue;
     }
     // the second job's units go to the pairs so that all have about the same
-    // number of steps, counting those of the first job
-    const auto steps = [&](int i) { return units[i] ? static_cast<double>(a.job[i].k_steps) * a.job[i].segments / a.job[i].splits : 0.0; };
+    // work, counting that of the first job
+    const auto steps = [&](int i) {
+        const Job& j = a.job[i];
+        return units[i] ? cost_of(static_cast<double>(j.k_steps) * j.segments / j.splits) : 0.0;
+    };
     const int64_t ahead = units[0] % pairs;                  // pairs that have one more unit of the first job
     a.late = static_cast<int32_t>(pairs - ahead);
     if (units[1]) {
@@ -892,9 +980,23 @@ cudaError_t launch_ff_forward(const q8_gated_ff& f, uint16_t* h, int64_t h_strid
         e = encode(d, &a.x, m[0], kStepK, a.columns);
         for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = encode(d, &a.w[i], m[1 + i], kStepK, kFewRows);
         if (e != cudaSuccess) return e;
-        few_kernel<<<static_cast<unsigned>(ceil_div(f.d_ff, kFewRows)), kFewThreads,
-                     1024 + a.stages * few_stage_bytes(a.columns), st>>>(a);
-        return cudaGetLastError();
+        const int64_t tiles = ceil_div(f.d_ff, kFewRows);
+        a.parts = 1;
+        // at least four stages to a part, and the parts fit where the stages were
+        while (a.parts < 8 && tiles * a.parts * 2 <= d.sms && a.k_steps >= 8 * a.parts &&
+               (2 * a.parts - 1) * a.columns * 512 + a.columns * kFewRows * 4 <= a.stages * few_stage_bytes(a.columns))
+            a.parts *= 2;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim = {static_cast<unsigned>(a.parts), 1, 1};
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.parts));
+        cfg.blockDim = dim3(kFewThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(1024 + a.stages * few_stage_bytes(a.columns));
+        cfg.stream = st;
+        cfg.attrs = &attr;
+        cfg.numAttrs = a.parts > 1;
+        return cudaLaunchKernelEx(&cfg, few_kernel, a);
     }
     TileArgs a{};
     if ((e = dual_args(f, d, m, &a)) != cudaSuccess) return e;

@@ -578,6 +578,11 @@ __global__ void __launch_bounds__(MAXT, 1) norm_backward_kernel(const __grid_con
         red.sum(t);
         return t[0];
     };
+    const auto reduce_two = [&](float2 a, float2 b) {
+        float t[2] = {a.x + a.y, b.x + b.y};
+        red.sum(t);
+        return make_float2(t[0], t[1]);
+    };
 
     Raw<uint16_t, VEC, E> y_next, dz_next{};
     Raw<R, VEC, E> r_next, dr_next{};
@@ -664,8 +669,13 @@ __global__ void __launch_bounds__(MAXT, 1) norm_backward_kernel(const __grid_con
                     add_dot(sd, e, rn[c]);
                     if (r_layer) add_all(sm, e);
                 }
-                if (n.pre_kind != Q8_NORM_NONE) dot = reduce(sd) * inv_dim;
-                if (r_layer) mean = reduce(sm) * inv_dim;
+                if (r_layer) {
+                    const float2 both_sums = reduce_two(sd, sm);
+                    dot = both_sums.x * inv_dim;
+                    mean = both_sums.y * inv_dim;
+                } else if (n.pre_kind != Q8_NORM_NONE) {
+                    dot = reduce(sd) * inv_dim;
+                }
             }
             // d, dr, and the gradient of the normalised y (kept in rn)
             float2 sd = both(0.0f), sm = both(0.0f);
@@ -695,8 +705,13 @@ __global__ void __launch_bounds__(MAXT, 1) norm_backward_kernel(const __grid_con
             }
             if (!g.d_y) continue;
             dot = mean = 0.0f;
-            if (n.post_kind != Q8_NORM_NONE) dot = reduce(sd) * inv_dim;
-            if (y_layer) mean = reduce(sm) * inv_dim;
+            if (y_layer) {
+                const float2 both_sums = reduce_two(sd, sm);
+                dot = both_sums.x * inv_dim;
+                mean = both_sums.y * inv_dim;
+            } else if (n.post_kind != Q8_NORM_NONE) {
+                dot = reduce(sd) * inv_dim;
+            }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Eight e = fma8(yn_of(c), -dot, y_layer ? rn[c] + -mean : rn[c]);
@@ -750,6 +765,11 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_staged_kernel(const __grid_co
         float t[1] = {s.x + s.y};
         red.sum(t);
         return t[0];
+    };
+    const auto reduce_two = [&](float2 a, float2 b) {
+        float t[2] = {a.x + a.y, b.x + b.y};
+        red.sum(t);
+        return make_float2(t[0], t[1]);
     };
     const auto fetch = [&](int64_t t, int stage) {
         const uint32_t bar = smem_addr(&s_full[stage]), to = smem_addr(stages + stage * stage_bytes);
@@ -854,13 +874,15 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_staged_kernel(const __grid_co
             if (n.pre_kind != Q8_NORM_NONE) {
                 s = both(0.0f);
                 add_dot(s, e, rn);
-                const float dot = reduce(s) * inv_dim;
                 if (r_layer) {
-                    s = both(0.0f);
-                    add_all(s, e);
-                    e = e + -(reduce(s) * inv_dim);
+                    float2 m = both(0.0f);
+                    add_all(m, e);
+                    s = reduce_two(s, m);
+                    e = e + -(s.y * inv_dim);
+                } else {
+                    s.x = reduce(s);
                 }
-                e = fma8(rn, -dot, e);
+                e = fma8(rn, -(s.x * inv_dim), e);
             }
             d = fma8(e, rs, d);
         }
@@ -880,13 +902,15 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_staged_kernel(const __grid_co
                 if (LAYER) d = masked<8>(d, 0, dim);
                 s = both(0.0f);
                 add_dot(s, d, yn);
-                const float dot = reduce(s) * inv_dim;
                 if (y_layer) {
-                    s = both(0.0f);
-                    add_all(s, d);
-                    d = d + -(reduce(s) * inv_dim);
+                    float2 m = both(0.0f);
+                    add_all(m, d);
+                    s = reduce_two(s, m);
+                    d = d + -(s.y * inv_dim);
+                } else {
+                    s.x = reduce(s);
                 }
-                d = fma8(yn, -dot, d) * y_rs;
+                d = fma8(yn, -(s.x * inv_dim), d) * y_rs;
             }
             put<8>(g.d_y + t * g.d_y_stride, dim, 0, d);
         }
@@ -904,53 +928,68 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_staged_kernel(const __grid_co
 }
 
 // What the CTAs have of each sum, added up: 32 columns to a block, its 16 warps
-// take every 16th CTA, and their sums are added in order.  blockIdx.y: the
-// weights' sums, then the gate's groups (or, where these are more than the CTAs,
-// the CTAs' ends: only a group that more than one CTA has rows of is summed
-// here).
+// take every 16th CTA, and their sums are added in order.  Blocks
+// [0, count * column blocks): the weights' sums.  Then the gate: only a group
+// that more than one CTA has rows of is summed here.  Where groups are fewer
+// than CTAs, the same for each group; else a block for each CTA's end, which a
+// group may reach over, with all columns.
 struct SumArgs {
     const float *partial, *gate_partial;
     uint16_t *out[kGate], *gate_out;
-    int64_t ctas, dim, tokens, gate_tokens;
+    int64_t ctas, dim, tokens, gate_tokens, column_blocks;
     int32_t count;                   // of the weights' sums
 };
 
 __global__ void __launch_bounds__(512) norm_sum_kernel(const __grid_constant__ SumArgs a)
 {
     __shared__ float part[16][33];
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x, dim = a.dim;
+    const int64_t dim = a.dim, block = blockIdx.x;
+    const int64_t col = block % a.column_blocks * 32 + threadIdx.x, which = block / a.column_blocks;
+    const auto first = [&](int64_t c) { return first_row(a.tokens, c, a.ctas); };
+    const float* p;
     uint16_t* out;
+    int64_t from = threadIdx.y, stop = a.ctas, step = dim;
     float s = 0.0f;
-    if (static_cast<int>(blockIdx.y) < a.count) {
-        const float* p = a.partial + blockIdx.y * a.ctas * dim + col;
-        if (col < dim) {
-#pragma unroll 8
-            for (int64_t c = threadIdx.y; c < a.ctas; c += 16) s += p[c * dim];
-        }
-        out = a.out[blockIdx.y];
+    if (which < a.count) {
+        p = a.partial + which * a.ctas * dim + col;
+        out = a.out[which];
     } else {
-        const int64_t y = blockIdx.y - a.count, groups = (a.tokens + a.gate_tokens - 1) / a.gate_tokens;
-        const auto first = [&](int64_t c) { return first_row(a.tokens, c, a.ctas); };
+        const int64_t groups = (a.tokens + a.gate_tokens - 1) / a.gate_tokens;
+        const bool few = groups < a.ctas;
         int64_t begin, cta;                          // the group's first row, and the CTA that has it
-        if (groups < a.ctas) {
-            begin = y * a.gate_tokens;               // below 2^40, the CTAs at most 2^14
-            cta = begin * a.ctas / a.tokens;         // or one beside it
+        if (few) {
+            begin = (which - a.count) * a.gate_tokens;       // below 2^40, the CTAs at most 2^14
+            cta = begin * a.ctas / a.tokens;                 // or one beside it
             while (cta + 1 < a.ctas && first(cta + 1) <= begin) ++cta;
             while (first(cta) > begin) --cta;
         } else {
-            cta = y;
+            cta = block - a.count * a.column_blocks;
             begin = first(cta + 1) / a.gate_tokens * a.gate_tokens;
             if (begin == first(cta + 1) || begin < first(cta)) return;
         }
         const int64_t end = min(begin + a.gate_tokens, a.tokens);
         if (cta + 1 == a.ctas || first(cta + 1) >= end) return;      // written by the CTA itself
+        stop = min(a.ctas, (end - 1) * a.ctas / a.tokens + 2);
+        while (first(stop - 1) >= end) --stop;
         // the first CTA's part lies in its second place unless the group is its first
-        if (col < dim) {
-            const float* p = a.gate_partial + col;
-            if (threadIdx.y == 0) s = p[(2 * cta + (first(cta) < begin)) * dim];
-            for (int64_t c = cta + 1 + threadIdx.y; c < a.ctas && first(c) < end; c += 16) s += p[2 * c * dim];
-        }
+        const float* head = a.gate_partial + (2 * cta + (first(cta) < begin)) * dim;
         out = a.gate_out + begin / a.gate_tokens * dim;
+        if (!few) {
+            for (int64_t c = threadIdx.y * 32 + threadIdx.x; c < dim; c += 512) {
+                s = head[c];
+                for (int64_t k = cta + 1; k < stop; ++k) s += a.gate_partial[2 * k * dim + c];
+                out[c] = float_to_bf16(s);
+            }
+            return;
+        }
+        if (threadIdx.y == 0 && col < dim) s = head[col];
+        p = a.gate_partial + col;
+        from += cta + 1;
+        step = 2 * dim;
+    }
+    if (col < dim) {
+#pragma unroll 8
+        for (int64_t c = from; c < stop; c += 16) s += p[c * step];
     }
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
@@ -1090,7 +1129,10 @@ Plan plan(const q8_block_norm& n, const q8_block_norm_grads& g, int sms)
         resident = std::max(1, s.most / p.threads);
     }
     resident = std::min<int64_t>({resident, 16, 228 * 1024 / (p.smem + 2048)});
-    p.ctas = std::min<int64_t>({n.tokens, kMostCtas, sms * std::max<int64_t>(1, resident)});
+    // past two CTAs to an SM, four rows to a CTA at least: each CTA's sums are
+    // written and read once more
+    p.ctas = std::min<int64_t>({n.tokens, kMostCtas, sms * std::max<int64_t>(1, resident),
+                                std::max<int64_t>(2 * sms, ceil_div(n.tokens, 4))});
     auto take = [&](int64_t floats) {
         const int64_t at = p.bytes;
         p.bytes += ceil_div(floats * 4, 256) * 256;
@@ -1185,15 +1227,17 @@ cudaError_t launch_norm_backward(const q8_block_norm& n, const q8_block_norm_gra
     if ((e = prepare_norm()) != cudaSuccess) return e;
     k<<<static_cast<unsigned>(p.ctas), p.threads, static_cast<size_t>(p.smem), st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    SumArgs s{a.partial, a.gate_partial, {}, g.d_gate, p.ctas, n.dim, n.tokens, std::max<int64_t>(1, n.gate_tokens), 0};
+    SumArgs s{a.partial, a.gate_partial, {}, g.d_gate, p.ctas, n.dim, n.tokens, std::max<int64_t>(1, n.gate_tokens),
+              ceil_div(n.dim, 32), 0};
     uint16_t* outs[kGate] = {g.d_post_weight, g.d_post_bias, g.d_pre_weight, g.d_pre_bias};
     for (uint16_t* o : outs)
         if (o) s.out[s.count++] = o;
-    int64_t ends = 0;                                        // of the gate's groups that may reach over two CTAs
-    if (g.d_gate && p.ctas > 1) ends = std::min(ceil_div(n.tokens, n.gate_tokens), p.ctas - 1);
-    if (s.count + ends > 0)
-        norm_sum_kernel<<<dim3(static_cast<unsigned>(ceil_div(n.dim, 32)), static_cast<unsigned>(s.count + ends)), dim3(32, 16), 0,
-                          st>>>(s);
+    int64_t blocks = s.count * s.column_blocks;
+    if (g.d_gate && p.ctas > 1 && n.gate_tokens > 1) {       // a group of one row has one CTA
+        const int64_t groups = ceil_div(n.tokens, n.gate_tokens);
+        blocks += groups < p.ctas ? groups * s.column_blocks : p.ctas - 1;
+    }
+    if (blocks) norm_sum_kernel<<<static_cast<unsigned>(blocks), dim3(32, 16), 0, st>>>(s);
     return cudaGetLastError();
 }
 
