@@ -453,12 +453,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 // a CTA has a tile, and two CTAs on an SM keep 200 KB of weights in flight.
 // Where tiles are fewer than half the SMs a cluster of 2, 4 or 8 CTAs shares a
 // tile's K and the first adds up the others' parts, which they write to its
-// shared memory (78 tokens, 2752 x 601, 10 tiles: 29 us alone, SPLIT us with
-// eight; with as many tiles as SMs parts only take the loads of a row apart:
-// 24 tokens, 2560 x 10240: 36 us with two).
+// shared memory (1 token, 1952 x 728: 10.8 us alone, 9 us with eight; with as
+// many tiles as SMs parts only take the loads of a row apart: 24 tokens,
+// 2560 x 10240: 36 us with two).
 // A lane of tensor memory is a column of g (0..63) or u (64..127): they meet
 // through shared memory.
-constexpr int kFewTokens = 128, kFewRows = 64, kFewThreads = 128, kFewStages = 8;
+constexpr int kFewTokens = 128, kFewRows = 64, kFewThreads = 256, kFewStages = 8;
 
 struct FewArgs {
     CUtensorMap x, w[2];
@@ -544,21 +544,23 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     ok = __all_sync(0xFFFFFFFFu, bar_wait(done, 0)) && ok;
     tc_fence_after();
 
-    // lane l < 64: column f0 + l of g; lane 64 + l: the same of u
-    const int l = (warp & 1) * 32 + lane;
+    // lane l < 64: column f0 + l of g; lane 64 + l: the same of u.  Warps 0..3 and
+    // 4..7 take every other 16 tokens.
+    const int quad = warp & 3, l = (quad & 1) * 32 + lane, side = quad >> 1;
     const int64_t f = static_cast<int64_t>(f0) + l;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     // over the stages, which nobody reads any more: the other CTAs' parts
     // [parts - 1][columns][128], then what the warps of g and those of u give one
     // another, [columns][64]
     float* s_part = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
     float* s_other = s_part + (args.parts - 1) * args.columns * 128;
+    const int c_first = (warp >> 2) * 16;
     float v[16];
     if (args.parts > 1) {
         cluster_sync();                              // all have read their stages
         if (part > 0) {
-            const uint32_t to = peer_addr(smem_addr(s_part + (part - 1) * args.columns * 128 + warp * 32 + lane), 0);
-            for (int c = 0; c < args.columns; c += 16) {
+            const uint32_t to = peer_addr(smem_addr(s_part + (part - 1) * args.columns * 128 + quad * 32 + lane), 0);
+            for (int c = c_first; c < args.columns; c += 32) {
                 tmem_load16(lanes + c, v);
                 tmem_load_wait();
 #pragma unroll
@@ -570,30 +572,37 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     } else {
         __syncthreads();
     }
-    const auto column = [&](int c) {
-        tmem_load16(lanes + c, v);
-        tmem_load_wait();
-        for (int p = 0; p < args.parts - 1; ++p)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += s_part[(p * args.columns + c + j) * 128 + warp * 32 + lane];
-    };
-    // the warps of g (0, 1) make h for the first half of the tokens, those of u for
-    // the second; each gives the other its values of the other's half first
-    const int side = warp >> 1;
-    const auto own = [&](int c) { return (2 * c >= args.columns) == (side == 1); };
+    // the warps of g make h for the first half of the tokens, those of u for the
+    // second; each gives the other its values of the other's half first
     for (int pass = 0; pass < 2 && part == 0; ++pass) {
-        for (int c = 0; c < args.columns; c += 16) {
-            if (own(c) != (pass == 1)) continue;
-            column(c);
+        for (int c = c_first; c < args.columns; c += 32) {
+            if (((2 * c >= args.columns) == (side == 1)) != (pass == 1)) continue;
+            tmem_load16(lanes + c, v);
+            tmem_load_wait();
+            for (int p = 0; p < args.parts - 1; ++p)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const bool in = c + j < args.tokens && f < args.d_ff;
-                if (in && args.save) args.save[(static_cast<int64_t>(side) * args.tokens + c + j) * args.d_ff + f] = v[j];
-                float* other = s_other + (c + j) * kFewRows + l;
-                if (pass == 0) *other = v[j];
-                else if (in)
-                    args.h[(c + j) * args.h_stride + f] =
-                        float_to_bf16(side ? act_value(*other, args.act) * v[j] : act_value(v[j], args.act) * *other);
+                for (int j = 0; j < 16; ++j) v[j] += s_part[(p * args.columns + c + j) * 128 + quad * 32 + lane];
+            float* other = s_other + c * kFewRows + l;
+            const int n = f < args.d_ff ? args.tokens - c : 0;       // of the 16 that exist
+            if (args.save) {
+                float* save = args.save + (static_cast<int64_t>(side) * args.tokens + c) * args.d_ff + f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j, save += args.d_ff)
+                    if (j < n) *save = v[j];
+            }
+            if (pass == 0) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) other[j * kFewRows] = v[j];
+            } else {
+                uint16_t* h = args.h + c * args.h_stride + f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float o = other[j * kFewRows];
+                    v[j] = act_value(side ? o : v[j], args.act) * (side ? v[j] : o);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j, h += args.h_stride)
+                    if (j < n) *h = float_to_bf16(v[j]);
             }
         }
         __syncthreads();
