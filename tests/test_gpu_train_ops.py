@@ -562,3 +562,45 @@ def test_loss_without_labels_weights_or_teacher(cuda_device):
     loss_check(got, loss_want(z, ids[:, :0], teacher[:, :0], labels, w, 1.0, 1.0, 1.0), w, z, 1.0, 1.0, 1.0)
     empty = torch.empty(0, device="cuda")
     q8.q8_distill_topk_forward(z[:0], ids[:0], teacher[:0], empty)
+
+
+# ------------------------------------------------- offsets that pass 32 bits
+
+def test_offsets_past_32_bits(cuda_device):
+    """More than 2^31 elements to a matrix: the last rows against the same rows alone."""
+    last = 40
+
+    T, V = 42800, 50257
+    z = torch.empty(T, V, dtype=BF, device="cuda").normal_(0, 2, generator=gen(1))
+    tail, ids, teacher, labels, w = loss_case(last, V, 9, False, seed=2)
+    z[-last:] = tail
+    all_ids = ids[torch.arange(T, device="cuda") % last]
+    all_ids[-last:] = ids
+    spread = lambda t: torch.cat([t[torch.arange(T - last, device="cuda") % last], t])
+    loss = torch.empty(T, device="cuda")
+    q8.q8_distill_topk_forward(z, all_ids, spread(teacher), loss, dlogits=z, labels=spread(labels), row_weight=spread(w),
+                               temperature=2.0, kd_weight=0.5, ce_weight=0.5)
+    got = (loss[-last:],) * 3 + (z[-last:],)
+    loss_check(got, loss_want(tail, ids, teacher, labels, w, 2.0, 0.5, 0.5), w, tail, 2.0, 0.5, 0.5)
+    del z, loss
+
+    T, D = 540000, 4096
+    c = norm_case(last, D, R.RMS, R.LAYER, 1, 0, False, seed=3)
+    big = {k: torch.empty(T, D, dtype=BF, device="cuda").normal_(0, 1, generator=gen(4)) for k in ("r", "y", "dr", "dz")}
+    for k, t in big.items():
+        t[-last:] = c[k]
+    kw = dict(post_weight=c["pw"], pre_weight=c["qw"])
+    q8.q8_block_norm_backward(big["r"], big["y"], big["dr"], big["dz"], big["dr"], big["dz"], R.RMS, R.LAYER, **kw)
+    z = torch.empty_like(big["y"])
+    q8.q8_block_norm_forward(big["r"], big["y"], big["r"], z, R.RMS, R.LAYER, **kw)
+    got = (big["r"][-last:], z[-last:], dict(r=big["dr"][-last:], y=big["dz"][-last:]))
+    want = norm_want(c, R.RMS, R.LAYER, last, 1.0, 1e-5)
+    norm_check(c, got, want, last, D, R.RMS, R.LAYER, last, 1.0, 1e-5)
+    del big, z
+
+    T, D, F = 135000, 64, 16384
+    x, wg, wu, dh = ff_case(T, D, F, seed=5)
+    got = ff_run(x, wg, wu, dh, q8.SILU, save=False)
+    want, tol = ff_bounds(x[-last:], wg, wu, dh[-last:], q8.SILU)
+    for k in ("h", "dx"):
+        close(got[k][-last:], want[k], tol[k], k)
