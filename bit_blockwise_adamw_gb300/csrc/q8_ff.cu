@@ -21,6 +21,11 @@
 // the pair's first CTA issues the products, eight warps run the epilogue from
 // tensor memory, whose 512 columns hold two accumulators, so that a tile's
 // epilogue runs under the next tile's products.
+//
+// The tensor cores bound it where tiles are many: 8192 tokens, 4096 x 16384,
+// forward and backward, 4.18 ms or 1.58 PFLOP/s, at the board's power limit.
+// With few tiles the last round does: 1023 tokens, 1600 x 6400, 121 us for
+// 63.7 us of products at their peak rate, 200 forward tiles on 76 pairs.
 #include <algorithm>
 #include <cmath>
 #include <map>
@@ -458,6 +463,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 // 2560 x 10240: 36 us with two).
 // A lane of tensor memory is a column of g (0..63) or u (64..127): they meet
 // through shared memory.
+// 24 tokens, 2560 x 10240: 22.8 us for 105 MB of weights, 4.6 TB/s (69 % of a
+// copy's rate); memory is read 128 bytes of a row at a time, and the ring's
+// first fill and the last epilogue have nothing to run under.
 constexpr int kFewTokens = 128, kFewRows = 64, kFewThreads = 256, kFewStages = 8;
 
 struct FewArgs {
@@ -655,7 +663,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     }
 }
 
-// dg and du from the saved g and u: eight columns of a row to a thread.
+// dg and du from the saved g and u: eight columns of a row to a thread.  g and u
+// are saved in 32 bits: dg and du are rounded once, as the products' operands,
+// and dx and dw are then 1.4 times as far from float64 as a float32 evaluation
+// (256 and 512 tokens, SiLU); with g and u rounded to 16 bits too, 1.8 times.
+// Bytes bound it where d_ff is large (14 an element, 8 of them the saved ones).
 __global__ void __launch_bounds__(256) gates_kernel(const float* save, const uint16_t* dh, int64_t dh_stride, int64_t M,
                                                     int64_t N, int act, uint16_t* dg, uint16_t* du, int64_t stride)
 {
