@@ -31,11 +31,14 @@
 #include <mutex>
 #include <tuple>
 
+#include "q8_distill_plan.h"
 #include "q8_internal.h"
 #include "q8_tc.cuh"
 #include "q8_train.h"
 
 namespace q8 {
+
+using namespace distill;
 
 namespace {
 
@@ -144,23 +147,7 @@ struct RowSpan {
     }
 };
 
-enum Mode { kForward, kTrain, kStream };
-
-constexpr int kMaxSlots = 16;
 constexpr int kDropped = 0x7FFFDEAD;  // marks, for a moment, an entry whose id an earlier one has (a NaN no conversion gives)
-constexpr int kTeachers = 3;         // rows whose teacher is held: one in pass 2, one in pass 1, one being prepared
-constexpr int kOwn = 64;             // threads beside those of the passes
-
-// The shapes of a CTA: threads of the passes, CTAs that fit on an SM, 16-byte
-// vectors of a chunk to a thread.  A row costs each warp some 300 instructions
-// beside its elements, so that a row has no more warps than it needs.
-enum Shape { kFifth, kHalf, kWhole };
-__host__ __device__ constexpr int threads_of(int shape) { return shape == kFifth ? 128 : 512; }
-__host__ __device__ constexpr int ctas_per_sm(int shape) { return shape == kFifth ? 5 : shape == kHalf ? 2 : 1; }
-template <typename T>
-__host__ __device__ constexpr int chunk_vectors(int shape) { return shape == kWhole ? 3 : sizeof(T) == 2 ? 4 : 2; }
-
-constexpr int kMaxCluster = 8;
 
 struct RowArgs {
     q8_distill_topk d;
@@ -215,7 +202,7 @@ __global__ void __launch_bounds__(threads_of(SHAPE) + kOwn, ctas_per_sm(SHAPE)) 
     using Span = RowSpan<T>;
     constexpr int kPer = Span::kPer;
     constexpr int NT = threads_of(SHAPE);
-    constexpr int kVecs = chunk_vectors<T>(SHAPE);
+    constexpr int kVecs = chunk_vectors(SHAPE, sizeof(T));
     constexpr int kWarps = NT / 32;
     const q8_distill_topk& d = args.d;
 
@@ -799,55 +786,6 @@ __global__ void __launch_bounds__(threads_of(SHAPE) + kOwn, ctas_per_sm(SHAPE)) 
 
 // ------------------------------------------------------------------------- host
 
-// Shared memory of an SM and the most of a CTA; 1 KB to each CTA is kept by the
-// system, 1.5 KB at most are static.
-constexpr int64_t kSm = 228 * 1024, kOfCta = 1024 + 1536;
-
-struct Config {
-    int mode = kForward;
-    int ctas = 1, shape = kHalf;     // CTAs to a row
-    int slots = 0, chunk = 0, seen = 0;
-    size_t smem = 0;
-};
-
-Config configure(const q8_distill_topk& d, bool grad, bool first_pass, int sms)
-{
-    const int64_t elem = d.logits_dtype == Q8_F32 ? 4 : 2;
-    const int64_t vecs = std::max<int64_t>(1, d.vocab * elem / 16);
-    Config c;
-    c.mode = !grad ? kForward : first_pass ? kTrain : kStream;
-    c.seen = 4;
-    while (c.seen < 2 * d.k) c.seen *= 2;
-    const int64_t teacher = (kTeachers * 16 + 24) * ((d.k + 4) & ~int64_t(3)) + 4 * c.seen;
-    const auto set = [&](int ctas, int shape) {
-        const int64_t share = (vecs + ctas - 1) / ctas;
-        const int64_t most = (elem == 4 ? chunk_vectors<float>(shape) : chunk_vectors<uint16_t>(shape)) * threads_of(shape);
-        c.ctas = ctas;
-        c.shape = shape;
-        c.chunk = static_cast<int>(std::min(share, most));
-        const int64_t chunks = (share + c.chunk - 1) / c.chunk;
-        const int64_t room = kSm / ctas_per_sm(shape) - kOfCta - teacher;
-        c.slots = static_cast<int>(std::min<int64_t>(kMaxSlots, room / (c.chunk * 16)));
-        c.smem = static_cast<size_t>(c.slots) * c.chunk * 16 + static_cast<size_t>(teacher);
-        // kTrain: all of a slice, one chunk more when the next row's has one more,
-        // and two ahead
-        return c.slots >= (c.mode == kTrain ? chunks + 3 : 2);
-    };
-    // Rows up to 16 KB: small CTAs, many of them on an SM.  kTrain: otherwise the
-    // smallest CTAs whose ring holds the row, and then more of them to a row.
-    bool fits = (vecs <= 1024 && set(1, kFifth)) || set(1, kHalf);
-    for (int n = 1; n <= kMaxCluster && !fits; n *= 2) fits = set(n, kWhole);
-    if (!fits) {
-        c.mode = kStream;
-        set(1, kHalf);
-    }
-    // few rows: more CTAs to each, while a slice stays at least 8 KB
-    int n = c.ctas;
-    while (n < kMaxCluster && d.rows * n * 2 <= sms && vecs / (2 * n) >= 512) n *= 2;
-    if (n > c.ctas) set(n, c.shape);
-    return c;
-}
-
 cudaError_t allow_shared(const void* kernel)
 {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -924,6 +862,7 @@ cudaError_t launch_distill(const q8_distill_topk& d, float* loss, float* stats_o
     if (e == cudaSuccess) e = earlier_fault(dev.fault);
     if (e != cudaSuccess) return e;
     const Config c = configure(d, dlogits != nullptr, stats_in == nullptr, dev.sms);
+    if (!c.usable) return cudaErrorInvalidConfiguration;
     const bool dual = d.kd_weight > 0.0f && d.ce_weight > 0.0f && d.temperature != 1.0f;
     const RowKernel k = row_kernel_of(d.logits_dtype == Q8_F32, c.mode, dual, c.shape);
     cudaLaunchAttribute attr{};
