@@ -552,6 +552,12 @@ __global__ void __launch_bounds__(threads_of(SHAPE) + kOwn, ctas_per_sm(SHAPE)) 
             }
         };
 
+        int b = 0;                                    // of the prepared teachers
+        uint32_t taught_phase = 0;
+        const auto next_teacher = [&]() {
+            if (++b == kTeachers) b = 0, taught_phase ^= 1;
+        };
+
         // The row's maximum and sums, from all threads of all CTAs.  Every thread
         // has then left the pass before it (one barrier).
         int parity = 0;
@@ -564,8 +570,12 @@ __global__ void __launch_bounds__(threads_of(SHAPE) + kOwn, ctas_per_sm(SHAPE)) 
             merge_lanes<DUAL>(m, kWarps, c1, ct);
             if (ranks > 1) {
                 // to every CTA of the cluster; a buffer is written again two rows
-                // on, after all have read it
+                // on, after all have read it.  The gradient may be written over
+                // the logits, and a teacher reads them anywhere in the row: a CTA
+                // tells the others to go on only when its own teacher is done
+                // (most rows' has been for a row)
                 if (tid < static_cast<int>(ranks)) {
+                    if (GRAD) wait(&s_taught[b], taught_phase);
                     const uint32_t to = peer_addr(smem_addr(&s_peer[parity][rank]), tid);
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(m.max) : "memory");
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(m.s1) : "memory");
@@ -686,11 +696,6 @@ __global__ void __launch_bounds__(threads_of(SHAPE) + kOwn, ctas_per_sm(SHAPE)) 
             if (e.at >= 0) store(r.out, e.at, slope1(s, e.z));
         };
 
-        int b = 0;
-        uint32_t taught_phase = 0;
-        const auto next_teacher = [&]() {
-            if (++b == kTeachers) b = 0, taught_phase ^= 1;
-        };
         Place read;                                   // of the pass that reads first
         if (MODE == kTrain) {
             Place write;                              // of pass 2
