@@ -854,12 +854,12 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_staged_kernel(const __grid_co
             Eight p = yn_of() * chunk_of(w, 0);
             if (n.post_bias) p = p + channels<8>(n.post_bias, dim, 0);
             rn = fma8(eight_r(at + 2 * half), n.residual_scale, p * chunk_of(gate, 0));
+            if (LAYER) rn = masked<8>(rn, 0, dim);       // past the row's end a layer norm of y leaves -mean
         }
         float rs = 1.0f;
         if (n.pre_kind != Q8_NORM_NONE) {
             if (r_layer) {
                 s = both(0.0f);
-                rn = masked<8>(rn, 0, dim);
                 add_all(s, rn);
                 rn = masked<8>(rn + -(reduce(s) * inv_dim), 0, dim);
             }

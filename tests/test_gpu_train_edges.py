@@ -6,6 +6,7 @@ import torch
 
 import bit_blockwise_adamw_gb300 as q8
 import test_gpu_train_ops as ops
+import train_refs as R
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,34 @@ def test_loss_over_the_logits_where_ctas_share_a_row(cuda_device, T, V, K, f32, 
     if T <= 8:
         want = ops.loss_want(z, ids, teacher, labels, w, tau, 0.8, 0.2)
         ops.loss_check((loss, loss, loss, d, d2), want, w, z, tau, 0.8, 0.2)
+
+
+# -------------------------------------------------------------------- block norms
+
+@pytest.mark.parametrize("T,D", [(5, 8), (700, 64), (9, 96), (33, 264), (21, 1600), (4, 4104), (3, 97)])
+@pytest.mark.parametrize("post,pre,rows", [(R.LAYER, R.RMS, 0), (R.LAYER, R.RMS, 1), (R.LAYER, R.LAYER, 0), (R.LAYER, R.NONE, 0),
+                                           (R.RMS, R.RMS, 0), (R.RMS, R.LAYER, 0), (R.NONE, R.LAYER, 0)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_without_weights_at_widths_that_threads_do_not_divide(cuda_device, T, D, post, pre, rows, f32):
+    """Columns that a thread has past the row's end count in no statistic, also
+    where no weight makes them zero."""
+    c = ops.norm_case(T, D, post, pre, 0, rows, f32, seed=T + D)
+    got = ops.norm_run(c, post, pre, T, 0.75, 1e-5)
+    ops.norm_check(c, got, ops.norm_want(c, post, pre, T, 0.75, 1e-5), T, D, post, pre, T, 0.75, 1e-5)
+
+
+@pytest.mark.parametrize("D", [64, 264])
+def test_norm_weights_gradients_without_weights(cuda_device, D):
+    """The gradients of weights and biases that are ones and zeros."""
+    T = 50
+    c = ops.norm_case(T, D, R.LAYER, R.RMS, 0, 0, False, seed=D)
+    one = dict(c, pw=torch.ones(D, dtype=BF, device="cuda"), pb=torch.zeros(D, dtype=BF, device="cuda"),
+               qw=torch.ones(D, dtype=BF, device="cuda"), qb=torch.zeros(D, dtype=BF, device="cuda"))
+    want = ops.norm_want(one, R.LAYER, R.RMS, T, 1.0, 1e-5)
+    got = {k: torch.empty(D, dtype=BF, device="cuda") for k in ("pw", "pb", "qw", "qb")}
+    dr, dy = torch.empty_like(c["r"]), torch.empty_like(c["y"])
+    q8.q8_block_norm_backward(c["r"], c["y"], c["dr"], c["dz"], dr, dy, R.LAYER, R.RMS, dpost_weight=got["pw"],
+                              dpost_bias=got["pb"], dpre_weight=got["qw"], dpre_bias=got["qb"])
+    out, z = torch.empty_like(c["r"]), torch.empty_like(c["y"])
+    q8.q8_block_norm_forward(c["r"], c["y"], out, z, R.LAYER, R.RMS)
+    ops.norm_check(one, (out, z, dict(got, r=dr, y=dy)), want, T, D, R.LAYER, R.RMS, T, 1.0, 1e-5)
