@@ -371,6 +371,13 @@ def _array(t: Optional[torch.Tensor], name: str, dtype, shape):
     return t.data_ptr()
 
 
+def _torch_stream(stream, like):
+    """The given stream for torch.cuda.stream(); None is the current one."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else torch.cuda.default_stream(like.device)
+
+
 def _workspace(fn, need, workspace, like, stream):
     """(address, bytes, the tensor that holds it): the caller's workspace, or
     one from torch's allocator for the stream that the call runs on."""
@@ -382,14 +389,8 @@ def _workspace(fn, need, workspace, like, stream):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if need == 0:
         return 0, 0, None
-    if stream is None:
+    with torch.cuda.stream(_torch_stream(stream, like)):
         t = torch.empty(need, dtype=torch.uint8, device=like.device)
-    else:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else \
-                torch.cuda.default_stream(like.device)
-        with torch.cuda.stream(stream):
-            t = torch.empty(need, dtype=torch.uint8, device=like.device)
     return t.data_ptr(), need, t
 
 
@@ -508,7 +509,8 @@ def q8_block_norm_backward(residual: torch.Tensor, y: torch.Tensor, dresidual_ou
                            dpost_weight=None, dpost_bias=None, dpre_weight=None, dpre_bias=None, dgate=None,
                            workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """The gradients of q8_block_norm_forward's inputs (each output may be
-    None) from those of its outputs (None: zeros)."""
+    None) from those of its outputs (None: zeros).  Rows of a gate that no
+    token has get a gradient of zeros: all of them where there are no tokens."""
     L = _lib or load_library()
     n = _block_norm(residual, y, post_kind, pre_kind, post_weight, post_bias, pre_weight, pre_bias, gate, gate_tokens,
                     residual_scale, eps)
@@ -528,6 +530,12 @@ def q8_block_norm_backward(residual: torch.Tensor, y: torch.Tensor, dresidual_ou
     rc = L.q8_block_norm_backward(n, _BLOCK_NORM_GRADS.pack(*g, wp, wb), _on(stream, y))
     if rc:
         _check("q8_block_norm_backward", rc)
+    if dgate is not None:
+        tokens, rows = shape[0], 1 if gate.dim() == 1 else gate.shape[0]
+        used = -(-tokens // gate_tokens) if gate_tokens else rows if tokens else 0       # what the call writes
+        if used < rows:
+            with torch.cuda.stream(_torch_stream(stream, y)):
+                dgate.view(rows, shape[1])[used:].zero_()
 
 
 def _distill(logits, teacher_ids, teacher_logits, labels, row_weight, temperature, kd_weight, ce_weight):

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import bit_blockwise_adamw_gb300 as q8
+from bit_blockwise_adamw_gb300 import nn as q8nn
 import test_gpu_train_ops as ops
 import train_refs as R
 
@@ -80,3 +81,40 @@ def test_norm_weights_gradients_without_weights(cuda_device, D):
     out, z = torch.empty_like(c["r"]), torch.empty_like(c["y"])
     q8.q8_block_norm_forward(c["r"], c["y"], out, z, R.LAYER, R.RMS)
     ops.norm_check(one, (out, z, dict(got, r=dr, y=dy)), want, T, D, R.LAYER, R.RMS, T, 1.0, 1e-5)
+
+
+def test_norm_gate_rows_without_tokens_get_zeros(cuda_device):
+    """A gate's gradient is written whole: zeros where no token has the row."""
+    D = 136
+    c = ops.norm_case(20, D, R.RMS, R.RMS, 1, 1, False, seed=1)
+    kw = dict(post_weight=c["pw"], pre_weight=c["qw"])
+    gate = torch.cat([c["gate"]] * 4)
+    for tokens, gate_tokens, used in ((20, 10, 2), (20, 7, 3), (20, 20, 1), (0, 5, 0), (0, None, 0)):
+        r, y, dr, dz = (c[k][:tokens] for k in ("r", "y", "dr", "dz"))
+        dgate, want = torch.full_like(gate, 9.0), torch.zeros_like(gate)
+        q8.q8_block_norm_backward(r, y, dr, dz, None, None, R.RMS, R.RMS, gate=gate, gate_tokens=gate_tokens, dgate=dgate, **kw)
+        if used:
+            q8.q8_block_norm_backward(r, y, dr, dz, None, None, R.RMS, R.RMS, gate=gate[:used].contiguous(),
+                                      gate_tokens=gate_tokens, dgate=want[:used], **kw)
+        assert torch.equal(dgate, want), (tokens, gate_tokens)
+    one = torch.full((D,), 9.0, dtype=BF, device="cuda")
+    q8.q8_block_norm_backward(r, y, dr, dz, None, None, R.RMS, R.RMS, gate=c["gate"][0], dgate=one, **kw)
+    assert not one.any()
+    side = torch.cuda.Stream()
+    one.fill_(9.0)
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        q8.q8_block_norm_backward(r, y, dr, dz, None, None, R.RMS, R.RMS, gate=c["gate"][0], dgate=one, stream=stream, **kw)
+    side.synchronize()
+    assert not one.any()
+
+
+def test_norm_no_tokens_through_autograd(cuda_device):
+    """Every parameter of the module has a gradient of zeros."""
+    m = q8nn.BlockNorm(64, post="layer", pre="rms", device="cuda")
+    torch.full((1 << 16,), 7.0, device="cuda")       # what the allocator gives next is not zero by chance
+    r = torch.zeros(2, 0, 64, dtype=BF, device="cuda", requires_grad=True)
+    out, z = m(r, torch.zeros_like(r))
+    assert out.shape == z.shape == r.shape
+    (out.sum() + z.sum()).backward()
+    assert all(p.grad is not None and not p.grad.any() for p in m.parameters())
