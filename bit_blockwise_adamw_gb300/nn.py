@@ -49,7 +49,7 @@ def gated_ff(x, w_gate, w_up, activation="silu", recompute=False):
     """act(x w_gate^T) * (x w_up^T), differentiable in all three.  Both
     projections are kept in float32 for the backward pass; recompute=True keeps
     nothing and computes them again there."""
-    return _GatedFF.apply(_flat(x), w_gate, w_up, ACTIVATIONS[activation], recompute).view(*x.shape[:-1], -1)
+    return _GatedFF.apply(_flat(x), w_gate, w_up, ACTIVATIONS[activation], recompute).view(*x.shape[:-1], w_gate.shape[0])
 
 
 class _BlockNorm(torch.autograd.Function):

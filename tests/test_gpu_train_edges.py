@@ -14,6 +14,16 @@ pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 
 
+# ------------------------------------------------------------ gated feed-forward
+
+def test_ff_no_tokens_through_autograd(cuda_device):
+    m = q8nn.GatedFeedForward(64, 136, device="cuda")
+    out = m(torch.zeros(2, 0, 64, dtype=BF, device="cuda", requires_grad=True))
+    assert out.shape == (2, 0, 64)
+    out.sum().backward()
+    assert all(p.grad is not None and not p.grad.any() for p in m.parameters())
+
+
 # ------------------------------------------------------------------- distillation
 
 @pytest.mark.parametrize("T", [4, 100])
