@@ -19,7 +19,7 @@ NORMS = {None: B.NORM_NONE, "none": B.NORM_NONE, "rms": B.NORM_RMS, "layer": B.N
 
 def _flat(t):
     """t as a matrix the operators take: rows of unit stride that do not overlap."""
-    t = t.reshape(-1, t.shape[-1])
+    t = t.reshape(t.shape[:-1].numel(), t.shape[-1])
     return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
 
 
@@ -119,12 +119,15 @@ class _DistillTopK(torch.autograd.Function):
 def distill_topk(logits, teacher_ids, teacher_logits, labels=None, temperature=1.0, kd_weight=1.0, ce_weight=0.0):
     """Each row's distillation loss in float32 (q8_distill_topk_forward): the
     teacher's top entries as torch.topk gives them (ids outside the vocabulary
-    are padding), labels outside it (-100) are not counted.  Differentiable in
-    the logits."""
+    are padding), labels outside it (-100) are not counted.  Without a teacher
+    (None for both) the labels' term is left.  Differentiable in the logits."""
+    if (teacher_ids is None) != (teacher_logits is None):
+        raise ValueError("teacher_ids and teacher_logits go together")
     rows = logits.shape[:-1]
-    loss = _DistillTopK.apply(_flat(logits), _flat(teacher_ids).contiguous(), _flat(teacher_logits).float().contiguous(),
-                              None if labels is None else labels.reshape(-1).contiguous(), float(temperature), float(kd_weight),
-                              float(ce_weight))
+    ids, teacher = (None, None) if teacher_ids is None else \
+        (_flat(teacher_ids).contiguous(), _flat(teacher_logits).float().contiguous())
+    loss = _DistillTopK.apply(_flat(logits), ids, teacher, None if labels is None else labels.reshape(-1).contiguous(),
+                              float(temperature), float(kd_weight), float(ce_weight))
     return loss.view(rows)
 
 

@@ -62,6 +62,16 @@ def test_loss_over_the_logits_where_ctas_share_a_row(cuda_device, T, V, K, f32, 
         ops.loss_check((loss, loss, loss, d, d2), want, w, z, tau, 0.8, 0.2)
 
 
+def test_loss_of_labels_alone_through_autograd(cuda_device):
+    z, ids, teacher, labels, w = ops.loss_case(6, 1000, 0, False, seed=3)
+    want = ops.loss_want(z, ids, teacher, labels, w, 1.0, 1.0, 0.5)
+    for given in ((None, None), (ids, teacher)):
+        zz = z.clone().requires_grad_()
+        loss = q8nn.distill_topk(zz, *given, labels=labels, ce_weight=0.5)
+        d, = torch.autograd.grad((loss * w).sum(), zz)
+        ops.loss_check((loss, loss, loss, d), want, w, z, 1.0, 1.0, 0.5)
+
+
 # -------------------------------------------------------------------- block norms
 
 @pytest.mark.parametrize("T,D", [(5, 8), (700, 64), (9, 96), (33, 264), (21, 1600), (4, 4104), (3, 97)])

@@ -33,3 +33,27 @@ def test_gated_ff_without_tokens(calls, shape):
     assert h.shape == (*shape[:-1], 24)
     h.sum().backward()
     assert calls.last("q8_gated_ff_backward") and x.grad.shape == x.shape and w.grad.shape == w.shape
+
+
+@pytest.mark.parametrize("teacher", ["none", "empty"])
+@pytest.mark.parametrize("lead", [(4,), (2, 3), ()])
+def test_distill_without_teacher_entries(calls, teacher, lead):
+    """The labels' term alone: no teacher, or one of no entries."""
+    logits = torch.zeros(*lead, 9, requires_grad=True)
+    ids, t = (None, None) if teacher == "none" else (torch.zeros(*lead, 0, dtype=torch.int64), torch.zeros(*lead, 0))
+    loss = q8nn.distill_topk(logits, ids, t, labels=torch.zeros(lead, dtype=torch.int64), ce_weight=1.0)
+    assert loss.shape == lead
+    loss.sum().backward()
+    rows = logits.numel() // 9
+    for name in ("q8_distill_topk_forward", "q8_distill_topk_backward"):
+        a, kw = calls.last(name)
+        assert a[0].shape == (rows, 9) and kw["labels"].shape == (rows,)
+        assert (a[1] is None and a[2] is None) if teacher == "none" else a[1].shape == a[2].shape == (rows, 0)
+
+
+def test_distill_wants_both_of_the_teacher_or_neither(calls):
+    logits = torch.zeros(4, 9)
+    for ids, t in ((torch.zeros(4, 2, dtype=torch.int64), None), (None, torch.zeros(4, 2))):
+        with pytest.raises(ValueError, match="teacher"):
+            q8nn.distill_topk(logits, ids, t)
+    assert not calls.made
