@@ -25,10 +25,10 @@ def _flat(t):
 
 class _GatedFF(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, act, recompute):
+    def forward(ctx, x, w_gate, w_up, act, keep):
         h = torch.empty(x.shape[0], w_gate.shape[0], dtype=x.dtype, device=x.device)
         saved = None
-        if not recompute and any(ctx.needs_input_grad[:3]):
+        if keep and any(ctx.needs_input_grad[:3]):
             saved = torch.empty(2, *h.shape, dtype=torch.float32, device=x.device)
         B.q8_gated_ff_forward(x, w_gate, w_up, h, act, saved=saved)
         ctx.save_for_backward(x, w_gate, w_up, saved)
@@ -49,7 +49,8 @@ def gated_ff(x, w_gate, w_up, activation="silu", recompute=False):
     """act(x w_gate^T) * (x w_up^T), differentiable in all three.  Both
     projections are kept in float32 for the backward pass; recompute=True keeps
     nothing and computes them again there."""
-    return _GatedFF.apply(_flat(x), w_gate, w_up, ACTIVATIONS[activation], recompute).view(*x.shape[:-1], w_gate.shape[0])
+    keep = not recompute and torch.is_grad_enabled()     # needs_input_grad is true of a parameter under no_grad, too
+    return _GatedFF.apply(_flat(x), w_gate, w_up, ACTIVATIONS[activation], keep).view(*x.shape[:-1], w_gate.shape[0])
 
 
 class _BlockNorm(torch.autograd.Function):
@@ -97,10 +98,10 @@ def block_norm(residual, y, post="rms", pre="rms", post_weight=None, post_bias=N
 
 class _DistillTopK(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, ids, teacher, labels, temperature, kd_weight, ce_weight):
+    def forward(ctx, logits, ids, teacher, labels, temperature, kd_weight, ce_weight, keep):
         rows = logits.shape[0]
         loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        stats = torch.empty(rows, 2, dtype=torch.float32, device=logits.device) if ctx.needs_input_grad[0] else None
+        stats = torch.empty(rows, 2, dtype=torch.float32, device=logits.device) if keep and ctx.needs_input_grad[0] else None
         ctx.opts = dict(temperature=temperature, kd_weight=kd_weight, ce_weight=ce_weight)
         B.q8_distill_topk_forward(logits, ids, teacher, loss, stats=stats, labels=labels, **ctx.opts)
         ctx.save_for_backward(logits, ids, teacher, labels, stats)
@@ -113,7 +114,7 @@ class _DistillTopK(torch.autograd.Function):
         d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         B.q8_distill_topk_backward(logits, ids, teacher, stats, d, labels=labels, row_weight=dloss.float().contiguous(),
                                    **ctx.opts)
-        return d, None, None, None, None, None, None
+        return d, None, None, None, None, None, None, None
 
 
 def distill_topk(logits, teacher_ids, teacher_logits, labels=None, temperature=1.0, kd_weight=1.0, ce_weight=0.0):
@@ -127,7 +128,7 @@ def distill_topk(logits, teacher_ids, teacher_logits, labels=None, temperature=1
     ids, teacher = (None, None) if teacher_ids is None else \
         (_flat(teacher_ids).contiguous(), _flat(teacher_logits).float().contiguous())
     loss = _DistillTopK.apply(_flat(logits), ids, teacher, None if labels is None else labels.reshape(-1).contiguous(),
-                              float(temperature), float(kd_weight), float(ce_weight))
+                              float(temperature), float(kd_weight), float(ce_weight), torch.is_grad_enabled())
     return loss.view(rows)
 
 

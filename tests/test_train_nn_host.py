@@ -57,3 +57,27 @@ def test_distill_wants_both_of_the_teacher_or_neither(calls):
         with pytest.raises(ValueError, match="teacher"):
             q8nn.distill_topk(logits, ids, t)
     assert not calls.made
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_nothing_is_kept_where_no_gradient_follows(calls, mode):
+    """Evaluation of a model whose parameters want gradients: no projections in
+    float32 beside h, no statistics beside the losses."""
+    m = q8nn.GatedFeedForward(8, 24)
+    logits = torch.zeros(4, 9, requires_grad=True)
+    with mode():
+        m(torch.zeros(3, 8, dtype=BF))
+        q8nn.distill_topk(logits, torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2))
+    assert calls.last("q8_gated_ff_forward")[1]["saved"] is None
+    assert calls.last("q8_distill_topk_forward")[1]["stats"] is None
+
+
+def test_what_a_backward_pass_needs_is_kept(calls):
+    m = q8nn.GatedFeedForward(8, 24)
+    m(torch.zeros(3, 8, dtype=BF))
+    assert calls.last("q8_gated_ff_forward")[1]["saved"].shape == (2, 3, 24)
+    q8nn.distill_topk(torch.zeros(4, 9, requires_grad=True), torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2))
+    assert calls.last("q8_distill_topk_forward")[1]["stats"].shape == (4, 2)
+    for kw in (dict(recompute=True), dict()):
+        q8nn.gated_ff(torch.zeros(3, 8, dtype=BF, requires_grad=bool(kw)), m.w_gate.detach(), m.w_up.detach(), **kw)
+        assert calls.last("q8_gated_ff_forward")[1]["saved"] is None
