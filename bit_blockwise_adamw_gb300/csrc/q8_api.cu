@@ -234,10 +234,12 @@ int q8_prepare_device(void)
     if (err == cudaSuccess) err = q8::prepare_step1();
     if (err == cudaSuccess) err = q8::prepare_step16();
     if (err == cudaSuccess) err = q8::prepare_codec();
-    if (err == cudaSuccess) err = q8::prepare_ff();
-    if (err == cudaSuccess) err = q8::prepare_norm();
-    if (err == cudaSuccess) err = q8::prepare_distill();
     if (err != cudaSuccess) return cuda_fail(err, "q8_prepare_device");
+    // The steps need none of what the training-step operators set up (a driver
+    // entry point, mapped host memory); where one fails, that operator's own
+    // calls try again and report it.
+    for (const auto prepare : {q8::prepare_ff, q8::prepare_norm, q8::prepare_distill})
+        if (prepare() != cudaSuccess) cudaGetLastError();
     return Q8_OK;
 }
 

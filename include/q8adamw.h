@@ -274,7 +274,8 @@ int q8_selftest_sqrt_div(uint64_t* counts, q8_stream_t stream);
  * out and caches the launch configuration of every kernel of the library on
  * this device.  Every other entry point does the part it needs on first use;
  * call this yourself before capturing a CUDA graph or when the first step
- * must not synchronise.
+ * must not synchronise.  A failure in the part of an operator of q8train.h,
+ * which the steps do not need, is left to that operator's own calls to report.
  */
 int q8_prepare_device(void);
 
