@@ -501,6 +501,41 @@ def q8_block_norm_forward(residual: torch.Tensor, y: torch.Tensor, residual_out:
         _check("q8_block_norm_forward", rc)
 
 
+def _block_norm_backward(residual, y, dresidual_out, dz, dresidual, dy, post_kind, pre_kind, post_weight, post_bias, pre_weight,
+                         pre_bias, gate, gate_tokens, residual_scale, eps, dpost_weight, dpost_bias, dpre_weight, dpre_bias,
+                         dgate):
+    """The norm's structure, and the fields of the gradients' before the workspace."""
+    n = _block_norm(residual, y, post_kind, pre_kind, post_weight, post_bias, pre_weight, pre_bias, gate, gate_tokens,
+                    residual_scale, eps)
+    shape, dtype = y.shape, residual.dtype
+    vec = (shape[1],)
+    rop, ros = (0, 0) if dresidual_out is None else _rows(dresidual_out, "dresidual_out", dtype, shape)
+    dzp, dzs = (0, 0) if dz is None else _rows(dz, "dz", _BF, shape)
+    drp, drs = (0, 0) if dresidual is None else _rows(dresidual, "dresidual", dtype, shape)
+    dyp, dys = (0, 0) if dy is None else _rows(dy, "dy", _BF, shape)
+    if dgate is not None and gate is None:
+        raise ValueError("dgate without a gate")
+    return n, (rop, dzp, drp, dyp, _array(dpost_weight, "dpost_weight", _BF, vec), _array(dpost_bias, "dpost_bias", _BF, vec),
+               _array(dpre_weight, "dpre_weight", _BF, vec), _array(dpre_bias, "dpre_bias", _BF, vec),
+               0 if dgate is None else _array(dgate, "dgate", _BF, gate.shape), ros, dzs, drs, dys)
+
+
+def q8_block_norm_workspace(residual: torch.Tensor, y: torch.Tensor, dresidual_out: Optional[torch.Tensor],
+                            dz: Optional[torch.Tensor], dresidual: Optional[torch.Tensor], dy: Optional[torch.Tensor],
+                            post_kind: int, pre_kind: int, post_weight=None, post_bias=None, pre_weight=None,
+                            pre_bias=None, gate=None, gate_tokens: Optional[int] = None, residual_scale: float = 1.0,
+                            eps: float = 1e-5, dpost_weight=None, dpost_bias=None, dpre_weight=None, dpre_bias=None,
+                            dgate=None) -> int:
+    """Bytes of workspace of q8_block_norm_backward with these arguments."""
+    n, g = _block_norm_backward(residual, y, dresidual_out, dz, dresidual, dy, post_kind, pre_kind, post_weight, post_bias,
+                                pre_weight, pre_bias, gate, gate_tokens, residual_scale, eps, dpost_weight, dpost_bias,
+                                dpre_weight, dpre_bias, dgate)
+    need = load_library().q8_block_norm_workspace(n, _BLOCK_NORM_GRADS.pack(*g, 0, 0))
+    if need < 0:
+        _check("q8_block_norm_workspace", need)
+    return need
+
+
 def q8_block_norm_backward(residual: torch.Tensor, y: torch.Tensor, dresidual_out: Optional[torch.Tensor],
                            dz: Optional[torch.Tensor], dresidual: Optional[torch.Tensor],
                            dy: Optional[torch.Tensor], post_kind: int, pre_kind: int, post_weight=None,
@@ -512,30 +547,20 @@ def q8_block_norm_backward(residual: torch.Tensor, y: torch.Tensor, dresidual_ou
     None) from those of its outputs (None: zeros).  Rows of a gate that no
     token has get a gradient of zeros: all of them where there are no tokens."""
     L = _lib or load_library()
-    n = _block_norm(residual, y, post_kind, pre_kind, post_weight, post_bias, pre_weight, pre_bias, gate, gate_tokens,
-                    residual_scale, eps)
-    shape, dtype = y.shape, residual.dtype
-    vec = (shape[1],)
-    rop, ros = (0, 0) if dresidual_out is None else _rows(dresidual_out, "dresidual_out", dtype, shape)
-    dzp, dzs = (0, 0) if dz is None else _rows(dz, "dz", _BF, shape)
-    drp, drs = (0, 0) if dresidual is None else _rows(dresidual, "dresidual", dtype, shape)
-    dyp, dys = (0, 0) if dy is None else _rows(dy, "dy", _BF, shape)
-    if dgate is not None and gate is None:
-        raise ValueError("dgate without a gate")
-    g = (rop, dzp, drp, dyp, _array(dpost_weight, "dpost_weight", _BF, vec), _array(dpost_bias, "dpost_bias", _BF, vec),
-         _array(dpre_weight, "dpre_weight", _BF, vec), _array(dpre_bias, "dpre_bias", _BF, vec),
-         0 if dgate is None else _array(dgate, "dgate", _BF, gate.shape), ros, dzs, drs, dys)
+    n, g = _block_norm_backward(residual, y, dresidual_out, dz, dresidual, dy, post_kind, pre_kind, post_weight, post_bias,
+                                pre_weight, pre_bias, gate, gate_tokens, residual_scale, eps, dpost_weight, dpost_bias,
+                                dpre_weight, dpre_bias, dgate)
     need = L.q8_block_norm_workspace(n, _BLOCK_NORM_GRADS.pack(*g, 0, 0))
     wp, wb, keep = _workspace("q8_block_norm_backward", need, workspace, y, stream)
     rc = L.q8_block_norm_backward(n, _BLOCK_NORM_GRADS.pack(*g, wp, wb), _on(stream, y))
     if rc:
         _check("q8_block_norm_backward", rc)
     if dgate is not None:
-        tokens, rows = shape[0], 1 if gate.dim() == 1 else gate.shape[0]
+        (tokens, dim), rows = y.shape, 1 if gate.dim() == 1 else gate.shape[0]
         used = -(-tokens // gate_tokens) if gate_tokens else rows if tokens else 0       # what the call writes
         if used < rows:
             with torch.cuda.stream(_torch_stream(stream, y)):
-                dgate.view(rows, shape[1])[used:].zero_()
+                dgate.view(rows, dim)[used:].zero_()
 
 
 def _distill(logits, teacher_ids, teacher_logits, labels, row_weight, temperature, kd_weight, ce_weight):

@@ -138,3 +138,22 @@ def test_norm_no_tokens_through_autograd(cuda_device):
     assert out.shape == z.shape == r.shape
     (out.sum() + z.sum()).backward()
     assert all(p.grad is not None and not p.grad.any() for p in m.parameters())
+
+
+@pytest.mark.parametrize("T,D", [(1000, 512), (50, 97), (3, 20001)])
+def test_norm_workspace_of_the_stated_size(cuda_device, T, D):
+    c = ops.norm_case(T, D, R.RMS, R.RMS, 1, 1, False, seed=D)
+    outs = dict(dpost_weight=torch.empty_like(c["pw"]), dgate=torch.empty_like(c["gate"]))
+    a = (c["r"], c["y"], c["dr"], c["dz"], torch.empty_like(c["r"]), torch.empty_like(c["y"]), R.RMS, R.RMS)
+    kw = dict(post_weight=c["pw"], pre_weight=c["qw"], gate=c["gate"], **outs)
+    need = q8.q8_block_norm_workspace(*a, **kw)
+    assert need > 0 and q8.q8_block_norm_workspace(c["r"][:0], c["y"][:0], None, None, None, None, R.RMS, R.RMS) == 0
+    q8.q8_block_norm_backward(*a, **kw)
+    want = [t.clone() for t in (a[4], a[5], *outs.values())]
+    room = torch.full((need + 256,), 7, dtype=torch.uint8, device="cuda")
+    q8.q8_block_norm_backward(*a, **kw, workspace=room[:need])
+    assert all(torch.equal(x, y) for x, y in zip((a[4], a[5], *outs.values()), want)) and (room[need:] == 7).all()
+    with pytest.raises(q8.Q8Error, match="workspace_bytes"):
+        q8.q8_block_norm_backward(*a, **kw, workspace=room[:need - 256])
+    with pytest.raises(q8.Q8Error, match="post_kind"):
+        q8.q8_block_norm_workspace(*a[:6], 7, R.RMS)
