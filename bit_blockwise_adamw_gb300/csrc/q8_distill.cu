@@ -827,9 +827,11 @@ using RowKernel = void (*)(RowArgs);
 template <typename T, int MODE>
 RowKernel row_kernel_of(bool dual, int shape)
 {
-    if (shape == kFifth) return dual ? row_kernel<T, MODE, true, kFifth> : row_kernel<T, MODE, false, kFifth>;
-    if (shape == kHalf || MODE != kTrain) return dual ? row_kernel<T, MODE, true, kHalf> : row_kernel<T, MODE, false, kHalf>;
-    return dual ? row_kernel<T, kTrain, true, kWhole> : row_kernel<T, kTrain, false, kWhole>;
+    switch (kernel_shape(MODE, shape)) {
+        case kFifth: return dual ? row_kernel<T, MODE, true, kFifth> : row_kernel<T, MODE, false, kFifth>;
+        case kHalf: return dual ? row_kernel<T, MODE, true, kHalf> : row_kernel<T, MODE, false, kHalf>;
+        default: return dual ? row_kernel<T, kTrain, true, kWhole> : row_kernel<T, kTrain, false, kWhole>;
+    }
 }
 
 RowKernel row_kernel_of(bool f32, int mode, bool dual, int shape)

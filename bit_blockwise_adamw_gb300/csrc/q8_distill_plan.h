@@ -32,6 +32,11 @@ Q8_BOTH constexpr int threads_of(int shape) { return shape == kFifth ? 128 : 512
 Q8_BOTH constexpr int ctas_per_sm(int shape) { return shape == kFifth ? 5 : shape == kHalf ? 2 : 1; }
 Q8_BOTH constexpr int chunk_vectors(int shape, int elem) { return shape == kWhole ? 3 : elem == 2 ? 4 : 2; }
 
+// The kernel that a CTA of that shape runs: loss and gradient from one call have
+// one for an SM to itself; otherwise such a CTA, which many entries leave no
+// half of an SM, runs that of the half.
+constexpr int kernel_shape(int mode, int shape) { return shape == kWhole && mode != kTrain ? kHalf : shape; }
+
 constexpr int kMaxCluster = 8;
 
 // Shared memory of an SM and the most of a CTA; 1 KB to each CTA is kept by the
@@ -57,7 +62,7 @@ inline Config configure(const q8_distill_topk& d, bool grad, bool first_pass, in
     const int64_t teacher = (kTeachers * 16 + 24) * ((d.k + 4) & ~int64_t(3)) + 4 * c.seen;
     const auto set = [&](int ctas, int shape) {
         const int64_t share = (vecs + ctas - 1) / ctas;
-        const int64_t most = chunk_vectors(shape, static_cast<int>(elem)) * threads_of(shape);
+        const int64_t most = chunk_vectors(kernel_shape(c.mode, shape), static_cast<int>(elem)) * threads_of(shape);
         c.ctas = ctas;
         c.shape = shape;
         c.chunk = static_cast<int>(std::min(share, most));

@@ -91,3 +91,23 @@ def test_wide_rows_with_many_entries(plan, rows, k):
     for vocab in (294920, 300000, 1 << 20):
         p = plan(rows, vocab, k, False, True, True)
         assert p["mode"] == STREAM and sound(p, vocab, k, False, True, True), p
+
+
+def test_chunks_are_those_of_the_kernel_that_runs(plan):
+    """Whole chunks are what the passes take unrolled: as many vectors to a
+    thread as the launched kernel is made for.  An SM to itself is a kernel of
+    its own only where loss and gradient come from one call; otherwise such a
+    CTA runs the half SM's."""
+    seen = set()
+    for vocab in (4096, 8192, 20000, 50257, 128256, 300000, 1 << 20):
+        for k in (0, 64, 500, 555, 600, 767, 900, 1024):
+            for f32 in (False, True):
+                for grad, first in WAYS:
+                    for rows in (1, 40, 8192):
+                        p = plan(rows, vocab, k, f32, grad, first)
+                        own = p["shape"] == WHOLE and p["mode"] == TRAIN
+                        whole = p["threads"] * (3 if own else 2 if f32 else 4)
+                        share = -(-(vocab * (4 if f32 else 2) // 16) // p["ctas"])
+                        assert p["chunk"] == min(share, whole), (rows, vocab, k, f32, p)
+                        seen.add((p["mode"], p["shape"]))
+    assert {(m, WHOLE) for m in (FORWARD, TRAIN, STREAM)} <= seen
