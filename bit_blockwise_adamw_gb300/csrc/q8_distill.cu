@@ -602,8 +602,10 @@ __global__ void __launch_bounds__(threads_of(SHAPE) + kOwn, ctas_per_sm(SHAPE)) 
             float part = 0.0f;
             if (r.taught)
                 for (int k = lane; k < K; k += 32) {
-                    const float l = logp[k];
-                    if (l > -INFINITY) part += expf(l) * (l - ((z[k] - m.max) * it - lst));
+                    // no weight adds nothing, also where l is finite and the student's
+                    // logit -inf
+                    const float l = logp[k], p = expf(l);
+                    if (p > 0.0f) part += p * (l - ((z[k] - m.max) * it - lst));
                 }
             for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
             if (lane == 0) {

@@ -169,7 +169,8 @@ int q8_block_norm_backward(const q8_block_norm* bn, const q8_block_norm_grads* g
  * entries (or K = 0) has no first term, one whose label lies outside
  * [0, vocab) no second: neither adds to its loss or gradient, and a row with
  * neither has loss 0 and a zero gradient.  An id that appears twice counts
- * twice.  A teacher logit of -inf has p_k = 0 and adds nothing; a student
+ * twice.  An entry whose p_k is 0 in fp32 (a teacher logit of -inf, or one some
+ * 104 tau below the largest) adds nothing; a student
  * logit of -inf has q_j = 0 (a row all of whose logits are -inf, or with NaN
  * or +inf among them, gives NaN).
  * labels NULL: no row has a label.  A term of weight 0 is not computed.

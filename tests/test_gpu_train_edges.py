@@ -1,6 +1,8 @@
 """Edges of the training-step operators on the GPU: sizes and calls at which a
 launch takes another shape, against the float64 forms and within the bounds of
 test_gpu_train_ops."""
+import math
+
 import pytest
 import torch
 
@@ -70,6 +72,26 @@ def test_loss_of_labels_alone_through_autograd(cuda_device):
         loss = q8nn.distill_topk(zz, *given, labels=labels, ce_weight=0.5)
         d, = torch.autograd.grad((loss * w).sum(), zz)
         ops.loss_check((loss, loss, loss, d), want, w, z, 1.0, 1.0, 0.5)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [500, 60000])
+def test_loss_entries_without_weight_on_masked_logits(cuda_device, V, f32):
+    """A teacher's entry so far below the others that its p is 0, on a student's
+    logit of -inf: it adds nothing to the loss, as an entry of -inf does."""
+    z, ids, teacher, labels, w = ops.loss_case(6, V, 8, f32, seed=V)
+    z[:, 300:] = -math.inf
+    ids[:] = torch.arange(296, 304, device="cuda")
+    teacher[:, 4:] = teacher[:, :1] - torch.tensor([1000.0, 500.0, 1e30, torch.finfo(torch.float32).max], device="cuda")
+    labels[:] = 5
+    none = teacher.clone()
+    none[:, 4:] = -math.inf
+    for tau, kd, ce in ((1.0, 1.0, 0.0), (2.0, 0.5, 0.5)):
+        got = ops.loss_run(z, ids, teacher, labels, w, tau, kd, ce)
+        assert torch.isfinite(got[0]).all()
+        want = ops.loss_want(z, ids, none, labels, w, tau, kd, ce)
+        zz = z.masked_fill(torch.isinf(z), 0.0)      # the bound's span is over the finite logits
+        ops.loss_check(got, want, w, zz, tau, kd, ce)
 
 
 # -------------------------------------------------------------------- block norms
