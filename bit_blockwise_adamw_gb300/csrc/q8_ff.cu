@@ -122,7 +122,8 @@ __device__ __forceinline__ float2 act_both(float g, int act)
         return make_float2(g * s, s * fmaf(g, 1.0f - s, 1.0f));
     }
     if (act == Q8_GELU_TANH) {
-        const float g2 = g * g, s = sigmoid(1.5957691216057308f * g * fmaf(0.044715f, g2, 1.0f));
+        // g^2 bounded: past 1e15 the sigmoid is 0 or 1, and infinity times s (1 - s) would be NaN
+        const float g2 = fminf(g * g, 1e30f), s = sigmoid(1.5957691216057308f * g * fmaf(0.044715f, g2, 1.0f));
         return make_float2(g * s, s + g * s * (1.0f - s) * 1.5957691216057308f * fmaf(0.134145f, g2, 1.0f));
     }
     const float cdf = normal_cdf(g);

@@ -26,6 +26,29 @@ def test_ff_no_tokens_through_autograd(cuda_device):
     assert all(p.grad is not None and not p.grad.any() for p in m.parameters())
 
 
+@pytest.mark.parametrize("act", [q8.SILU, q8.GELU_TANH, q8.GELU])
+@pytest.mark.parametrize("save", [True, False])
+def test_ff_projections_far_past_the_activations_bend(cuda_device, act, save):
+    """g of either sign up to 2^100 (its square is past fp32's range): act is g or
+    0, its derivative 1 or 0, and nothing is NaN."""
+    n = 64
+    x = torch.zeros(n, 64, dtype=BF, device="cuda")
+    exponent = torch.linspace(20, 100, n // 2).round()
+    x[:, 0] = torch.cat([2 ** exponent, -2 ** exponent]).to(BF)
+    x[:, 1] = 1.0
+    wg, wu = (torch.zeros(64, 64, dtype=BF, device="cuda") for _ in range(2))
+    wg[:, 0], wu[:, 1] = 1.0, 1.0
+    dh = torch.zeros(n, 64, dtype=BF, device="cuda")
+    dh[:, 0] = 1.0
+    got = ops.ff_run(x, wg, wu, dh, act, save)
+    up = (x[:, :1] > 0).to(BF)
+    assert torch.equal(got["h"], (x[:, :1] * up).expand(n, 64))
+    assert torch.equal(got["dx"][:, :2], torch.cat([up, x[:, :1] * up], 1)) and not got["dx"][:, 2:].any()
+    # dw_up's first element is the sum of the squares, past the type's range
+    assert torch.isfinite(got["dwg"]).all() and torch.isinf(got["dwu"][0, 0])
+    assert torch.isfinite(got["dwu"].flatten()[1:]).all()
+
+
 # ------------------------------------------------------------------- distillation
 
 @pytest.mark.parametrize("T", [4, 100])
