@@ -83,9 +83,16 @@ struct TileArgs {
     int32_t* fault;                  // host-mapped: set when a wait ran out
 };
 
-// act(g) and act'(g).  __expf and __fdividef are within a few units of 2^-23 of
-// their results where these do not vanish.
-__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
+// act(g) and act'(g).  __expf and the reciprocal are within a few units of 2^-23
+// of their results; the reciprocal also of subnormal ones, where __fdividef gives
+// 0 (past a denominator of 2^126): times the tanh form's inner derivative, some
+// hundreds there, such a result is a normal number.
+__device__ __forceinline__ float sigmoid(float t)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-t)));
+    return r;
+}
 
 // Phi(g) = erfc(-g / sqrt(2)) / 2, with erfc(z) = t exp(-z^2 + P(t)),
 // t = 1 / (1 + z / 2), z >= 0: the Chebyshev fit of Press et al., "Numerical

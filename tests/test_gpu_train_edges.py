@@ -49,6 +49,45 @@ def test_ff_projections_far_past_the_activations_bend(cuda_device, act, save):
     assert torch.isfinite(got["dwu"].flatten()[1:]).all()
 
 
+@pytest.mark.parametrize("act", [q8.SILU, q8.GELU_TANH, q8.GELU])
+@pytest.mark.parametrize("save", [True, False])
+def test_ff_activations_tails_relatively(cuda_device, act, save):
+    """g from -12.5 to -4, where act is small: every value within its rounding to
+    bf16 relatively, and the mean error of each stretch of g within what is left
+    when the roundings (RMS each, independent) cancel.  In fp32 the exponential's
+    argument comes to at most 90 with four roundings, 90 * 4 * 2^-24 relative in
+    the result, and __expf to 2 + 1.17 * 90 units of 2^-23: together below 2^-14.
+    g is a sum of two exact products, each within ACC of it."""
+    T, F, few, tiny = 512, 256, 2.0 ** -14, 2.0 ** -120
+    x = torch.zeros(T, 64, dtype=BF, device="cuda")
+    wg, wu = (torch.zeros(F, 64, dtype=BF, device="cuda") for _ in range(2))
+    x[:, 0], x[:, 1], x[:, 2] = torch.linspace(-12.4, -4.1, T), 1.0, 1.0
+    wg[:, 0], wg[:, 2], wu[:, 1] = 1.0, torch.linspace(-0.05, 0.05, F), 1.0
+    dh = torch.zeros(T, F, dtype=BF, device="cuda")
+    dh[:, 0] = 1.0
+    got = ops.ff_run(x, wg, wu, dh, act, save)
+    g = (x.double() @ wg.double().T).requires_grad_()
+    want = R.act(g, act) if act != q8.GELU else 0.5 * g * torch.special.erfc(-g * 0.5 ** 0.5)
+    if act == q8.GELU_TANH:                          # (1 + tanh t) / 2 without its cancellation
+        want = g * torch.sigmoid(2 * (2 / math.pi) ** 0.5 * (g + 0.044715 * g ** 3))
+    slope, = torch.autograd.grad(want.sum(), g, create_graph=True)
+    bend, = torch.autograd.grad(slope.sum(), g)
+    want, slope, g = want.detach(), slope.detach(), g.detach()
+    eg = 2 * ops.ACC * g.abs()
+    ops.close(got["h"], want, (ops.U + few) * want.abs() + slope.abs() * eg + tiny, "h")
+    # one column of dh: dx's first two columns are the one dg and du, rounded once
+    ops.close(got["dx"][:, 0], slope[:, 0], (ops.U + 2 * few) * slope[:, 0].abs() + bend[:, 0].abs() * eg[:, 0] + tiny, "dg")
+    ops.close(got["dx"][:, 1], want[:, 0], (ops.U + few) * want[:, 0].abs() + slope[:, 0].abs() * eg[:, 0] + tiny, "du")
+    normal = want.abs() > 2.0 ** -100
+    off = ((got["h"].double() - want) / want)
+    for lo in range(-13, -4):
+        at = (g >= lo) & (g < lo + 1) & normal
+        n = int(at.sum())
+        if n >= 1000:
+            slack = few + float((slope.abs() * eg / want.abs())[at].mean()) + 6 * ops.RMS / n ** 0.5
+            assert abs(float(off[at].mean())) <= slack, (lo, n, slack)
+
+
 # ------------------------------------------------------------------- distillation
 
 @pytest.mark.parametrize("T", [4, 100])
