@@ -88,6 +88,19 @@ def test_ff_activations_tails_relatively(cuda_device, act, save):
             assert abs(float(off[at].mean())) <= slack, (lo, n, slack)
 
 
+def test_ff_weights_gradients_over_more_than_2_31_elements(cuda_device):
+    """dw sums over every token of dg and du of 135000 x 16384: the first and the
+    last weights' rows against float64."""
+    T, D, F, n = 135000, 64, 16384, 24
+    x, wg, wu, dh = ops.ff_case(T, D, F, seed=6)
+    got = ops.ff_run(x, wg, wu, dh, q8.SILU, save=False)
+    for rows in (slice(0, n), slice(F - n, F)):
+        want, tol = ops.ff_bounds(x, wg[rows], wu[rows], dh[:, rows], q8.SILU)
+        for k in ("dwg", "dwu"):
+            ops.close(got[k][rows], want[k], tol[k], k)
+        ops.close(got["h"][:, rows], want["h"], tol["h"], "h")
+
+
 # ------------------------------------------------------------------- distillation
 
 @pytest.mark.parametrize("T", [4, 100])
