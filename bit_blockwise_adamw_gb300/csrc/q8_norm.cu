@@ -8,8 +8,8 @@
 // variance from the deviations, not from a difference of sums).  Bytes bound
 // both directions: forward 8, backward 12 bytes an element in bf16.  16384 x
 // 4096: forward 85 us, 6.3 TB/s (93 % of a copy's rate); backward with RMS norms
-// and 8 gates 228 us, 3.5 TB/s, held back by shared memory (the sums' reads and
-// writes) and by the wait for four reductions a row.
+// and 8 gates 228 us, 3.5 TB/s: four reductions a row, one after another, and the
+// sums' reads and writes in shared memory; no unit is above 62 %, it waits.
 //
 // The backward kernels recompute both norms from r and y and sum the weights'
 // gradients over its rows, in shared memory (each column has one thread, so
@@ -332,8 +332,12 @@ __host__ __device__ __forceinline__ int64_t first_row(int64_t tokens, int64_t c,
 
 // The backward kernel works on eight elements (a chunk) at a time, in packed
 // fp32 pairs: what it keeps of a row between its reductions is y, dz and dr' as
-// they came and one fp32 value an element, so that E = 16 fits in 128 registers
-// beside the next row's loads.
+// they came and one fp32 value an element.  Beside the next row's loads that is
+// more than 128 registers at E = 16 (140 to 360 bytes a thread are spilled with
+// vectors, 788 to 1006 with single elements) and far more than 64 at the wider
+// shapes (624 to 4438 bytes): it takes the rows that the staged kernel below
+// does not.  RMS, bf16: 4096 x 16384 452 us, 2048 x 32768 1359 us (120 us of
+// bytes each), 12007 x 4097 1560 us (88 us).
 struct Eight {
     float2 v[4];
 };

@@ -203,7 +203,10 @@ int q8_distill_topk_forward(const q8_distill_topk* d, float* loss, float* stats,
                             int64_t dlogits_stride, q8_stream_t stream);
 
 /* dlogits alone, from the forward call's stats; row_weight is the gradient of
- * the losses.  dlogits may be the logits themselves. */
+ * the losses.  dlogits may be the logits themselves.  A logsumexp is one rounded
+ * float, so that q_j and softmax(s)_j are off by about |logsumexp| * 2^-24 of
+ * themselves (logits over tau in the hundreds: some 2^-16); the forward call's
+ * own dlogits works relative to the row's maximum and is not. */
 int q8_distill_topk_backward(const q8_distill_topk* d, const float* stats, void* dlogits,
                              int64_t dlogits_stride, q8_stream_t stream);
 
