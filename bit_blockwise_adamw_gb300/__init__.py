@@ -10,7 +10,9 @@ from ._binding import (  # noqa: F401
     BLOCK, DISTILL_MAX_K, EXPORTS, GELU, GELU_TANH, MAX_STEP, NORM_LAYER, NORM_MAX_DIM, NORM_NONE, NORM_RMS,
     SIGNED, SILU, SMALL_NUMEL, UNSIGNED, HParams, LionHParams, MomentumHParams, Q8Error, Tensor16, Tensor8,
     adamw8bit_sr_step, adamw_bf16_sr_step, hparams, library_path, lion8bit_sr_step, lion_hparams, load_library,
-    momentum8bit_sr_step, momentum_hparams, pack_tensor16, pack_tensor8, q8_abi_version, q8_block_norm_backward,
-    q8_block_norm_forward, q8_block_norm_workspace, q8_blockwise_dequantize, q8_blockwise_quantize, q8_codebook_init,
-    q8_distill_topk_backward, q8_distill_topk_forward, q8_gated_ff_backward, q8_gated_ff_forward,
-    q8_gated_ff_workspace, q8_last_error, q8_philox_fill, q8_prepare_device, q8_selftest_sqrt_div)
+    momentum8bit_sr_step, momentum_hparams, pack_grads, pack_tensor16, pack_tensor8, q8_abi_version,
+    q8_block_norm_backward, q8_block_norm_forward, q8_block_norm_workspace, q8_blockwise_dequantize,
+    q8_blockwise_quantize, q8_clip_grads, q8_codebook_init, q8_distill_topk_backward, q8_distill_topk_forward,
+    q8_embedding_backward, q8_embedding_forward, q8_embedding_workspace, q8_gated_ff_backward, q8_gated_ff_forward,
+    q8_gated_ff_workspace, q8_grad_norm, q8_grad_norm_workspace, q8_last_error, q8_philox_fill, q8_prepare_device,
+    q8_selftest_sqrt_div)

@@ -35,7 +35,9 @@ EXPORTS = ("q8_codebook_init", "q8_blockwise_quantize", "q8_blockwise_dequantize
            "q8_philox_fill", "q8_selftest_sqrt_div", "q8_prepare_device", "q8_last_error", "q8_abi_version",
            "q8_gated_ff_workspace", "q8_gated_ff_forward", "q8_gated_ff_backward",
            "q8_block_norm_forward", "q8_block_norm_workspace", "q8_block_norm_backward",
-           "q8_distill_topk_forward", "q8_distill_topk_backward")
+           "q8_distill_topk_forward", "q8_distill_topk_backward",
+           "q8_embedding_forward", "q8_embedding_workspace", "q8_embedding_backward",
+           "q8_grad_norm_workspace", "q8_grad_norm", "q8_clip_grads")
 
 
 class Q8Error(RuntimeError):
@@ -85,6 +87,8 @@ _GATED_FF = struct.Struct("PPPqqqqPqi4x")
 _BLOCK_NORM = struct.Struct("PPPPPPPqqqqqiiiff4x")
 _BLOCK_NORM_GRADS = struct.Struct("PPPPPPPPPqqqqPq")
 _DISTILL_TOPK = struct.Struct("PPPPPqqqqifff")
+_EMBEDDING = struct.Struct("Pqqqif")
+_GRAD = struct.Struct("PPqii")
 
 
 _lib = None
@@ -126,6 +130,12 @@ def load_library(path: Optional[str] = None):
     L.q8_block_norm_backward.argtypes = [P, P, S]
     L.q8_distill_topk_forward.argtypes = [P, P, P, P, C.c_int64, S]
     L.q8_distill_topk_backward.argtypes = [P, P, P, C.c_int64, S]
+    L.q8_embedding_forward.argtypes = [P, P, P, C.c_int64, S]
+    L.q8_embedding_workspace.argtypes = [P]
+    L.q8_embedding_backward.argtypes = [P, P, C.c_int64, P, C.c_int, P, C.c_int64, S]
+    L.q8_grad_norm_workspace.argtypes = [C.c_int]
+    L.q8_grad_norm.argtypes = [P, C.c_int, P, P, C.c_int64, S]
+    L.q8_clip_grads.argtypes = [P, C.c_int, C.c_double, P, P, C.c_int64, S]
     for name in EXPORTS:
         if name.endswith("_workspace"):
             getattr(L, name).restype = C.c_int64
@@ -609,3 +619,153 @@ def q8_distill_topk_backward(logits: torch.Tensor, teacher_ids: Optional[torch.T
     rc = L.q8_distill_topk_backward(d, sp, gp, gs, _on(stream, logits))
     if rc:
         _check("q8_distill_topk_backward", rc)
+
+
+_device = torch._C._cuda_getDevice
+
+
+def _run(fn, like, *args):
+    """The library's call on like's device, which is the current one as a rule."""
+    L = _lib or load_library()
+    if like.get_device() == _device():
+        rc = getattr(L, fn)(*args)
+    else:
+        with torch.cuda.device(like.device):
+            rc = getattr(L, fn)(*args)
+    if rc:
+        _check(fn, rc)
+
+
+def _embedding(ids, rows, name, vocab, dim, scale):
+    """The structure, and (address, row stride) of out or dout."""
+    dtype = _dtype(rows, name)
+    if ids.dim() != 1:
+        raise ValueError("ids must be a contiguous %s CUDA array of one dimension" % _I64)
+    tokens = ids.shape[0]
+    ip = _array(ids, "ids", _I64, (tokens,))
+    return _EMBEDDING.pack(ip, tokens, vocab, dim, dtype, scale), *_rows(rows, name, rows.dtype, (tokens, dim))
+
+
+def _together(a, b, c):
+    if not a.get_device() == b.get_device() == c.get_device():
+        raise ValueError("the tensors of one call must be on one device")
+
+
+def _table(t, name):
+    """Address of a contiguous bf16 table [vocab, dim]."""
+    if t.dim() != 2:
+        raise ValueError("%s must be a %s CUDA matrix" % (name, _BF))
+    return _array(t, name, _BF, t.shape)
+
+
+def q8_embedding_forward(ids: torch.Tensor, table: torch.Tensor, out: torch.Tensor, scale: float = 1.0, stream=None) -> None:
+    """out[t] = scale * table[ids[t]] (bf16 or float32 [tokens, dim]); rows of
+    zeros where ids (int64 [tokens]) lies outside the table."""
+    tp = _table(table, "table")
+    e, op, os_ = _embedding(ids, out, "out", *table.shape, scale)
+    _together(ids, table, out)
+    _run("q8_embedding_forward", out, e, tp, op, os_, _on(stream, out))
+
+
+def q8_embedding_workspace(ids: torch.Tensor, dout: torch.Tensor, dtable: torch.Tensor) -> int:
+    """Bytes of workspace of q8_embedding_backward with these arguments."""
+    _table(dtable, "dtable")
+    e, _, _ = _embedding(ids, dout, "dout", *dtable.shape, 1.0)
+    need = load_library().q8_embedding_workspace(e)
+    if need < 0:
+        _check("q8_embedding_workspace", need)
+    return need
+
+
+def q8_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, dtable: torch.Tensor, scale: float = 1.0,
+                          accumulate: bool = False, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dtable[v] = scale * (the sum of dout's rows whose id is v): all of the
+    table, or with accumulate added to the rows that tokens have."""
+    L = _lib or load_library()
+    gp = _table(dtable, "dtable")
+    e, dp, ds = _embedding(ids, dout, "dout", *dtable.shape, scale)
+    need = L.q8_embedding_workspace(e)
+    _together(ids, dout, dtable)
+    wp, wb, keep = _workspace("q8_embedding_backward", need, workspace, dout, stream)
+    _run("q8_embedding_backward", dout, e, dp, ds, gp, int(accumulate), wp, wb, _on(stream, dout))
+
+
+class Grads:
+    """A list of gradients (and of where their clipped forms go) as the library
+    takes it: keep it to pass the same tensors again."""
+    __slots__ = ("bytes", "count", "like", "tensors", "clips")
+
+    def __init__(self, grads, out=None):
+        self.tensors = (list(grads), None if out is None else list(out))
+        self.clips = out is not None
+        grads, out = self.tensors
+        self.count, self.like = len(grads), grads[0] if grads else None
+        kinds = self._kinds(grads, "gradients")
+        sizes = list(map(torch.Tensor.numel, grads))
+        ptrs = list(map(torch.Tensor.data_ptr, grads))
+        if out is None:
+            outs, okinds = ptrs, kinds
+        else:
+            okinds = self._kinds(out, "out")
+            if list(map(torch.Tensor.numel, out)) != sizes:
+                raise ValueError("out must hold a tensor of each gradient's number of elements")
+            outs = list(map(torch.Tensor.data_ptr, out))
+        pack = _GRAD.pack
+        self.bytes = b"".join(map(pack, ptrs, outs, sizes, kinds, okinds))
+
+    def _kinds(self, tensors, name):
+        """Each tensor's q8_dtype."""
+        try:
+            kinds = [_DTYPES[t.dtype] for t in tensors]
+        except KeyError:
+            raise ValueError("%s must be bfloat16 or float32" % name) from None
+        if not all(map(torch.Tensor.is_contiguous, tensors)):
+            raise ValueError("%s must be contiguous" % name)
+        if tensors and (not self.like.is_cuda or set(map(torch.Tensor.get_device, tensors)) != {self.like.get_device()}):
+            raise ValueError("%s must be CUDA tensors of one device" % name)
+        return kinds
+
+
+def pack_grads(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None) -> Grads:
+    """The list for q8_grad_norm and q8_clip_grads, kept by a program whose
+    gradients stay where they are.  out: where the clipped gradients go (by
+    default over the gradients)."""
+    return Grads(grads, out)
+
+
+def _grads_call(fn, grads, norm, workspace, stream, *args):
+    L = _lib or load_library()
+    np_ = _array(norm, "norm", _F32, norm.shape)
+    if norm.numel() != 1:
+        raise ValueError("norm must hold one float32")
+    if grads.like is not None and grads.like.get_device() != norm.get_device():
+        raise ValueError("norm must be on the gradients' device")
+    need = L.q8_grad_norm_workspace(grads.count)
+    wp, wb, keep = _workspace(fn, need, workspace, norm, stream)
+    _run(fn, norm, grads.bytes, grads.count, *args, np_, wp, wb, _on(stream, norm))
+
+
+def q8_grad_norm_workspace(count: int) -> int:
+    """Bytes of workspace of q8_grad_norm and q8_clip_grads on so many gradients."""
+    need = load_library().q8_grad_norm_workspace(count)
+    if need < 0:
+        _check("q8_grad_norm_workspace", need)
+    return need
+
+
+def q8_grad_norm(grads, norm: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """norm (float32, one element): the 2-norm of all gradients together (a
+    list of bf16 and float32 tensors, or pack_grads of one)."""
+    _grads_call("q8_grad_norm", grads if isinstance(grads, Grads) else Grads(grads), norm, workspace, stream)
+
+
+def q8_clip_grads(grads, max_norm: float, norm: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradients times min(1, max_norm / (norm + 1e-6)), in place or into
+    out's tensors (bf16 or float32 each); norm as by q8_grad_norm."""
+    if isinstance(grads, Grads):
+        if out is not None:
+            raise ValueError("out is part of the packed list")
+    else:
+        grads = Grads(grads, out)
+    _grads_call("q8_clip_grads", grads, norm, workspace, stream, max_norm)

@@ -238,7 +238,7 @@ int q8_prepare_device(void)
     // The steps need none of what the training-step operators set up (a driver
     // entry point, mapped host memory); where one fails, that operator's own
     // calls try again and report it.
-    for (const auto prepare : {q8::prepare_ff, q8::prepare_norm, q8::prepare_distill})
+    for (const auto prepare : {q8::prepare_ff, q8::prepare_norm, q8::prepare_distill, q8::prepare_embed, q8::prepare_grads})
         if (prepare() != cudaSuccess) cudaGetLastError();
     return Q8_OK;
 }

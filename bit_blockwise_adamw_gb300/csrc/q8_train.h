@@ -15,6 +15,8 @@ namespace q8 {
 cudaError_t prepare_ff();
 cudaError_t prepare_norm();
 cudaError_t prepare_distill();
+cudaError_t prepare_embed();
+cudaError_t prepare_grads();
 
 // The current device's SM count, and the host-mapped word that a kernel sets
 // when one of its waits ran out.
@@ -49,6 +51,16 @@ cudaError_t launch_norm_backward(const q8_block_norm& n, const q8_block_norm_gra
 // forward: loss non-NULL; backward alone: loss NULL, stats read.
 cudaError_t launch_distill(const q8_distill_topk& d, float* loss, float* stats_out, const float* stats_in,
                            void* dlogits, int64_t dlogits_stride, cudaStream_t st);
+
+cudaError_t launch_embed_forward(const q8_embedding& e, const uint16_t* table, void* out, int64_t out_stride, cudaStream_t st);
+int64_t embed_workspace(const q8_embedding& e);
+cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64_t dout_stride, uint16_t* dtable,
+                                  bool accumulate, void* workspace, cudaStream_t st);
+
+int64_t grads_workspace(int count);
+// clip: out is written; else the norm alone.
+cudaError_t launch_grads(const q8_grad* list, int count, bool clip, double max_norm, float* norm, void* workspace,
+                         cudaStream_t st);
 
 __device__ __forceinline__ float bf16_to_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 

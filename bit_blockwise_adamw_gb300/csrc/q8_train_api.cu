@@ -126,6 +126,50 @@ int check_distill(const q8_distill_topk* d)
     return Q8_OK;
 }
 
+int check_embedding(const q8_embedding* e)
+{
+    if (!e) return fail(Q8_ERR_NULL, "q8_embedding is NULL");
+    if (e->tokens < 0 || e->tokens >= kMaxSize) return fail(Q8_ERR_SIZE, "tokens must lie in [0, 2^30)");
+    if (e->vocab < 1 || e->vocab >= (int64_t(1) << 31)) return fail(Q8_ERR_SIZE, "vocab must lie in [1, 2^31)");
+    if (e->dim < 1 || e->dim >= kMaxSize) return fail(Q8_ERR_SIZE, "dim must lie in [1, 2^30)");
+    if (e->dtype != Q8_BF16 && e->dtype != Q8_F32) return fail(Q8_ERR_ARG, "dtype must be Q8_BF16 or Q8_F32");
+    if (!std::isfinite(e->scale)) return fail(Q8_ERR_ARG, "scale must be finite");
+    if (e->tokens > 0 && !e->ids) return fail(Q8_ERR_NULL, "ids is NULL");
+    if (!aligned(e->ids, 8)) return fail(Q8_ERR_ALIGN, "ids must be 8-byte aligned");
+    return Q8_OK;
+}
+
+std::string entry(const char* what, int i) { return std::string(what) + " (gradient " + std::to_string(i) + ")"; }
+
+int check_grads(const q8_grad* list, int count, bool clip)
+{
+    if (count < 0) return fail(Q8_ERR_SIZE, "count must be >= 0");
+    if (count > 0 && !list) return fail(Q8_ERR_NULL, "list is NULL");
+    for (int i = 0; i < count; ++i) {
+        const q8_grad& g = list[i];
+        if (g.numel < 0 || g.numel >= kMaxTokens) return fail(Q8_ERR_SIZE, entry("numel must lie in [0, 2^40)", i));
+        if (g.grad_dtype != Q8_BF16 && g.grad_dtype != Q8_F32)
+            return fail(Q8_ERR_ARG, entry("grad_dtype must be Q8_BF16 or Q8_F32", i));
+        if (clip && g.out_dtype != Q8_BF16 && g.out_dtype != Q8_F32)
+            return fail(Q8_ERR_ARG, entry("out_dtype must be Q8_BF16 or Q8_F32", i));
+        if (g.numel == 0) continue;
+        if (!g.grad) return fail(Q8_ERR_NULL, entry("grad is NULL", i));
+        if (!aligned(g.grad, g.grad_dtype == Q8_F32 ? 4 : 2)) return fail(Q8_ERR_ALIGN, entry("grad is not aligned to its elements", i));
+        if (!clip) continue;
+        if (!g.out) return fail(Q8_ERR_NULL, entry("out is NULL", i));
+        if (!aligned(g.out, g.out_dtype == Q8_F32 ? 4 : 2)) return fail(Q8_ERR_ALIGN, entry("out is not aligned to its elements", i));
+        if (g.out == g.grad && g.out_dtype != g.grad_dtype) return fail(Q8_ERR_ARG, entry("out over grad must have grad's type", i));
+    }
+    return Q8_OK;
+}
+
+int check_norm_output(const float* norm)
+{
+    if (!norm) return fail(Q8_ERR_NULL, "norm is NULL");
+    if (!aligned(norm, 4)) return fail(Q8_ERR_ALIGN, "norm must be 4-byte aligned");
+    return Q8_OK;
+}
+
 std::mutex g_lock;
 std::map<int, q8::DeviceInfo> g_devices;
 
@@ -266,6 +310,70 @@ int q8_distill_topk_backward(const q8_distill_topk* d, const float* stats, void*
         return rc;
     const cudaError_t err = q8::launch_distill(*d, nullptr, nullptr, stats, dlogits, dlogits_stride, stream);
     return err == cudaSuccess ? Q8_OK : cuda_fail(err, "q8_distill_topk_backward launch");
+}
+
+int q8_embedding_forward(const q8_embedding* e, const uint16_t* table, void* out, int64_t out_stride,
+                         q8_stream_t stream)
+{
+    int rc = check_embedding(e);
+    if (rc == Q8_OK) rc = check_rows(table, 2, e->vocab, e->dim, e->dim, "table");
+    if (rc == Q8_OK) rc = check_rows(out, e->dtype == Q8_F32 ? 4 : 2, e->tokens, e->dim, out_stride, "out");
+    if (rc != Q8_OK || e->tokens == 0) return rc;
+    const cudaError_t err = q8::launch_embed_forward(*e, table, out, out_stride, stream);
+    return err == cudaSuccess ? Q8_OK : cuda_fail(err, "q8_embedding_forward launch");
+}
+
+int64_t q8_embedding_workspace(const q8_embedding* e)
+{
+    const int rc = check_embedding(e);
+    return rc != Q8_OK ? rc : q8::embed_workspace(*e);
+}
+
+int q8_embedding_backward(const q8_embedding* e, const void* dout, int64_t dout_stride, uint16_t* dtable,
+                          int accumulate, void* workspace, int64_t workspace_bytes, q8_stream_t stream)
+{
+    int rc = check_embedding(e);
+    if (rc != Q8_OK) return rc;
+    if (accumulate != 0 && accumulate != 1) return fail(Q8_ERR_ARG, "accumulate must be 0 or 1");
+    if ((rc = check_rows(dout, e->dtype == Q8_F32 ? 4 : 2, e->tokens, e->dim, dout_stride, "dout")) != Q8_OK) return rc;
+    if ((rc = check_rows(dtable, 2, e->vocab, e->dim, e->dim, "dtable")) != Q8_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, q8::embed_workspace(*e))) != Q8_OK) return rc;
+    cudaError_t err = cudaSuccess;
+    if (e->tokens == 0) {                        // sums over no tokens
+        if (!accumulate) err = cudaMemsetAsync(dtable, 0, static_cast<size_t>(e->vocab) * e->dim * 2, stream);
+    } else {
+        err = q8::launch_embed_backward(*e, dout, dout_stride, dtable, accumulate != 0, workspace, stream);
+    }
+    return err == cudaSuccess ? Q8_OK : cuda_fail(err, "q8_embedding_backward launch");
+}
+
+int64_t q8_grad_norm_workspace(int count)
+{
+    if (count < 0) return fail(Q8_ERR_SIZE, "count must be >= 0");
+    return q8::grads_workspace(count);
+}
+
+int q8_grad_norm(const q8_grad* list, int count, float* norm, void* workspace, int64_t workspace_bytes,
+                 q8_stream_t stream)
+{
+    int rc = check_grads(list, count, false);
+    if (rc == Q8_OK) rc = check_norm_output(norm);
+    if (rc == Q8_OK) rc = check_workspace(workspace, workspace_bytes, q8::grads_workspace(count));
+    if (rc != Q8_OK) return rc;
+    const cudaError_t err = q8::launch_grads(list, count, false, 0.0, norm, workspace, stream);
+    return err == cudaSuccess ? Q8_OK : cuda_fail(err, "q8_grad_norm launch");
+}
+
+int q8_clip_grads(const q8_grad* list, int count, double max_norm, float* norm, void* workspace,
+                  int64_t workspace_bytes, q8_stream_t stream)
+{
+    int rc = check_grads(list, count, true);
+    if (rc == Q8_OK && !(max_norm >= 0.0)) rc = fail(Q8_ERR_ARG, "max_norm must be >= 0");
+    if (rc == Q8_OK) rc = check_norm_output(norm);
+    if (rc == Q8_OK) rc = check_workspace(workspace, workspace_bytes, q8::grads_workspace(count));
+    if (rc != Q8_OK) return rc;
+    const cudaError_t err = q8::launch_grads(list, count, true, max_norm, norm, workspace, stream);
+    return err == cudaSuccess ? Q8_OK : cuda_fail(err, "q8_clip_grads launch");
 }
 
 }  // extern "C"

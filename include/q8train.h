@@ -5,7 +5,10 @@
  *    product), forward and backward;
  *  - the norms after a block and before the next one, fused with the block's
  *    gate and the residual scale, forward and backward;
- *  - distillation from a teacher's top logits, forward and backward.
+ *  - distillation from a teacher's top logits, forward and backward;
+ *  - the token embedding: lookup with a scale, and the gradient of its table;
+ * and what stands between the backward pass and those steps:
+ *  - the norm of all gradients, and their clipping.
  *
  * The conventions of q8adamw.h hold (device pointers owned by the caller, BF16
  * as 16-bit patterns, asynchronous work on `stream`, negative q8_status on
@@ -209,6 +212,76 @@ int q8_distill_topk_forward(const q8_distill_topk* d, float* loss, float* stats,
  * own dlogits works relative to the row's maximum and is not. */
 int q8_distill_topk_backward(const q8_distill_topk* d, const float* stats, void* dlogits,
                              int64_t dlogits_stride, q8_stream_t stream);
+
+/* ----------------------------------------------------------- token embedding
+ *
+ * With a table W [vocab, dim] (bf16, contiguous, as torch.nn.Embedding keeps
+ * it) and a token id for each of `tokens` rows:
+ *   out[t] = scale * W[ids[t]]                                  [tokens, dim]
+ * and for the gradient dout of out:
+ *   dW[v] = scale * (sum of dout[t] over the t with ids[t] = v)  [vocab, dim].
+ * An id outside [0, vocab) is no token: its row of out is zeros, and its row of
+ * dout is not read.  out and dout have the type dtype.  The sum of a table row
+ * is fp32, over the tokens' order in an association that depends on ids alone.
+ * 0 <= tokens < 2^30, 1 <= vocab < 2^31, 1 <= dim < 2^30, scale finite.
+ */
+typedef struct {
+    const int64_t* ids;        /* [tokens]                                   */
+    int64_t tokens, vocab, dim;
+    int32_t dtype;             /* q8_dtype                                   */
+    float scale;
+} q8_embedding;
+
+int q8_embedding_forward(const q8_embedding* e, const uint16_t* table, void* out, int64_t out_stride,
+                         q8_stream_t stream);
+
+/* Bytes of workspace of the backward call (it may be 0); negative: the
+ * q8_status of a bad argument. */
+int64_t q8_embedding_workspace(const q8_embedding* e);
+
+/* accumulate 0: all of dtable is written, zeros in rows that no token has.
+ * accumulate 1: the sums are added to what dtable holds (a table that is also
+ * the output layer's weight, or a further micro-batch; one rounding of each
+ * result), and rows that no token has are neither read nor written. */
+int q8_embedding_backward(const q8_embedding* e, const void* dout, int64_t dout_stride, uint16_t* dtable,
+                          int accumulate, void* workspace, int64_t workspace_bytes, q8_stream_t stream);
+
+/* --------------------------------------- norm of all gradients, and clipping
+ *
+ * Over a list of `count` gradients g_i (host array), as one flat vector:
+ *   norm = sqrt(sum over i, j of g_ij^2)
+ *   c = min(1, max_norm / (norm + 1e-6)),  out_ij = c * g_ij.
+ * Squares are summed in fp32 over at most 128 elements, scaled by a power of
+ * two where they would leave fp32's range, and then in double, so that no norm
+ * below 2^128 overflows and none above 2^-140 is lost; `norm` is rounded once,
+ * and so is c.  With an infinite gradient the norm is infinite and c is 0
+ * (infinite elements then give NaN); with NaN both are NaN and all results are.
+ * grad and out are contiguous, on their elements' own alignment; out may be
+ * grad itself where both have one type, and out_dtype may differ from
+ * grad_dtype elsewhere.  Clipping in place with c = 1 writes nothing.
+ * numel 0 entries are skipped.  0 <= count, 0 <= numel < 2^40; max_norm >= 0
+ * (it may be infinite: c is then 1 or NaN).
+ */
+typedef struct {
+    const void* grad;
+    void* out;                 /* q8_grad_norm: not used                     */
+    int64_t numel;
+    int32_t grad_dtype;        /* q8_dtype                                   */
+    int32_t out_dtype;         /* q8_dtype; q8_grad_norm: not used           */
+} q8_grad;
+
+/* Bytes of workspace of either call on a list of `count` entries; negative:
+ * the q8_status of a bad argument. */
+int64_t q8_grad_norm_workspace(int count);
+
+/* norm: device float[1]. */
+int q8_grad_norm(const q8_grad* list, int count, float* norm, void* workspace, int64_t workspace_bytes,
+                 q8_stream_t stream);
+
+/* norm: device float[1], the norm before clipping.  Nothing synchronises with
+ * the host: c is formed on the device. */
+int q8_clip_grads(const q8_grad* list, int count, double max_norm, float* norm, void* workspace,
+                  int64_t workspace_bytes, q8_stream_t stream);
 
 #ifdef __cplusplus
 }
