@@ -399,8 +399,11 @@ def _workspace(fn, need, workspace, like, stream):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if need == 0:
         return 0, 0, None
-    with torch.cuda.stream(_torch_stream(stream, like)):
+    if stream is None:                                   # entering a stream's context costs 12 us, for the current one, too
         t = torch.empty(need, dtype=torch.uint8, device=like.device)
+    else:
+        with torch.cuda.stream(_torch_stream(stream, like)):
+            t = torch.empty(need, dtype=torch.uint8, device=like.device)
     return t.data_ptr(), need, t
 
 

@@ -4,13 +4,19 @@
 // norm = sqrt(sum g^2), c = min(1, max_norm / (norm + 1e-6)), out = c * g: two
 // operations an element, so both are bound by the gradients' bytes.
 //
-// A list travels as kernel parameters, kMaxGrads tensors to a launch.  It is
-// cut into chunks of kChunk elements; each CTA takes a contiguous run of them
-// and leaves one sum of squares in the workspace, in double; whoever needs the
-// norm adds these up in one fixed order.
+// A list travels as kernel parameters, kMaxGrads tensors to a launch.  Each
+// tensor is cut into chunks of 32 KB that start on 16 bytes (the few
+// elements before the first and behind the last whole vector of eight go one by
+// one); each CTA takes a contiguous run of the launch's chunks and leaves one
+// sum of squares in the workspace, in double; whoever needs the norm adds these
+// up in one fixed order, without double arithmetic.  Clipping reads the gradients a second time, each CTA
+// its own run from the end backwards, so that what was read last, and is still
+// in L2, comes first.
 #include <algorithm>
-#include <memory>
+#include <cfloat>
+#include <cmath>
 
+#include "q8_device.cuh"
 #include "q8_internal.h"
 #include "q8_train.h"
 
@@ -19,10 +25,20 @@ namespace q8 {
 namespace {
 
 constexpr int kGradThreads = 256;
-constexpr int kOwnElems = 64;                              // elements that a thread adds up in fp32
-constexpr int kChunk = kGradThreads * kOwnElems;
+constexpr int kVecElems = 8;
+// Vectors that a thread has in flight: 128 bytes of either type.
+template <typename T> constexpr int kVecs = 16 / sizeof(T);
+template <typename T> constexpr int kChunk = kGradThreads * kVecElems * kVecs<T>;
+constexpr int kChunkBytes = kGradThreads * 128;
+constexpr int kKeepBytes = 60 << 20;                  // of L2's 126 MB
+constexpr int kPerSm = 4;                                  // CTAs of an SM
 constexpr int kMaxGrads = 768;
 constexpr int kMaxParts = 1024;                            // CTAs of one launch, at most
+
+// A launch's time on the host grows with its parameters: short lists travel in
+// short ones, with room for so many tensors (a norm of 64 tensors takes the host
+// 7.9 us instead of 9.3).
+constexpr int kFewGrads = 64;
 
 struct Grad {
     const void* g;
@@ -30,123 +46,455 @@ struct Grad {
     int64_t n;
 };
 
+// How a tensor's elements lie: the first `lead` come before a 16-byte boundary.
+enum : uint8_t { kF32 = 1, kOutF32 = 2, kOutVec = 4 };     // kOutVec: out's vectors start on 16 bytes, too
+struct Kind {
+    uint8_t flags, lead;
+};
+
+template <int ROOM>
 struct GradArgs {
     double* parts;             // sums of squares: kMaxParts of each launch
     float* norm;
-    double max_norm;
     int64_t nchunks;
+    float max_norm;
+    int32_t keep;              // chunks of a CTA's run that L2 is to keep for the second pass
     int32_t nt;
     int32_t parts_at;          // this launch's place in parts
     int32_t nparts;            // all launches' sums
-    int64_t start[kMaxGrads + 1];
-    uint8_t f32[kMaxGrads];    // bit 0: g is float32; bit 1: out is
-    Grad d[kMaxGrads];
+    uint16_t at[kMaxParts + 1];            // the tensor that each CTA's run of chunks begins in
+    int64_t start[ROOM + 1];               // each tensor's first chunk
+    Kind kind[ROOM];
+    Grad d[ROOM];
 };
-static_assert(sizeof(GradArgs) <= 32764, "kernel parameter space");
+static_assert(sizeof(GradArgs<kMaxGrads>) <= 32764, "kernel parameter space");
 
-__device__ __forceinline__ int find(const int64_t* start, int nt, int64_t chunk)
-{
-    int lo = 0, hi = nt;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (start[mid] <= chunk) lo = mid; else hi = mid;
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_float(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t* p, float x) { *p = float_to_bf16(x); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+
+// Eight elements as they lie in memory: one 16-byte vector of bf16, two of float32.
+template <typename T>
+struct Eight {
+    static constexpr int kWords = sizeof(T) / 2;
+    uint4 w[kWords];
+
+    // Loads that clipping may write over.  KEEP: L2 is to keep the line; else it
+    // is the first to go.
+    template <bool KEEP>
+    __device__ __forceinline__ void read(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = KEEP ? reinterpret_cast<const uint4*>(p)[i] : __ldcs(reinterpret_cast<const uint4*>(p) + i);
     }
-    return lo;
+    __device__ __forceinline__ float2 pair(int i) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t x = i == 0 ? w[0].x : i == 1 ? w[0].y : i == 2 ? w[0].z : w[0].w;
+            return bf16x2(x);
+        } else {
+            const uint4& v = w[i / 2];
+            return i % 2 ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void add_squares(const Eight<T>& v, float2 (&sum)[2])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = v.pair(i);
+        sum[i % 2] = __ffma2_rn(x, x, sum[i % 2]);
+    }
 }
 
-__device__ __forceinline__ float load(const void* p, bool f32, int64_t i)
+// The squares of a thread's vectors p, p + kGradThreads * 8, ... before `stop`
+// again, where their sum shows that some may have left fp32's range: the largest
+// magnitude picks a power of two that brings all of them, or all that count,
+// back into it.  Out of line, and read again, so that the loop that hardly ever
+// comes here keeps its registers.
+template <typename T>
+__device__ __noinline__ double squares_scaled(const T* p, const T* stop)
 {
-    return f32 ? static_cast<const float*>(p)[i] : bf16_to_float(static_cast<const uint16_t*>(p)[i]);
+    uint32_t top = 0;
+    for (const T* q = p; q < stop; q += kGradThreads * kVecElems)
+        for (int i = 0; i < kVecElems; ++i) top = max(top, __float_as_uint(load1(q + i)) & 0x7FFFFFFFu);
+    const int exponent = static_cast<int>(top >> 23) - 127;
+    if (top == 0) return 0.0;
+    const int k = exponent == 128 ? 0 : max(-126, min(126, -exponent));       // infinity and NaN stay what they are
+    const float scale = __int_as_float((127 + k) << 23);
+    float sum = 0.0f;
+    for (const T* q = p; q < stop; q += kGradThreads * kVecElems)
+        for (int i = 0; i < kVecElems; ++i) {
+            const float x = __fmul_rn(load1(q + i), scale);
+            sum = __fmaf_rn(x, x, sum);
+        }
+    return static_cast<double>(sum) * __longlong_as_double(static_cast<int64_t>(1023 - 2 * k) << 52);
 }
 
-__device__ double block_sum(double x, double* s)
+// A thread's sum of squares: hi + lo in fp32, lo what hi's roundings lost (Knuth's
+// two-sum), and what came out of range for them in double.  This GPU adds 64
+// floats in the time of one double: sums in double alone cost 6 us of a clipping
+// of 8 MB.
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;
+    double rare = 0.0;
+    bool any = false;
+
+    __device__ __forceinline__ void add(float x)
+    {
+        const float t = __fadd_rn(hi, x), b = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
+        hi = t;
+    }
+    // 2^90 leaves room for 2^36 summands
+    static __device__ __forceinline__ bool in_range(float s) { return s >= 0x1p-70f && s <= 0x1p90f; }
+    __device__ __forceinline__ void add_rare(double x)
+    {
+        rare += x;
+        any = true;
+    }
+    // One element's square.
+    __device__ __forceinline__ void add1(float x)
+    {
+        const float s = __fmul_rn(x, x);
+        if (in_range(s)) add(s);
+        else if (x != 0.0f) add_rare(static_cast<double>(x) * static_cast<double>(x));
+    }
+};
+
+template <bool KEEP, typename T>
+__device__ __forceinline__ void chunk_squares(Sum& total, const T* g, int64_t n, int lead, int64_t chunk)
 {
-    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(~0u, x, o);
-    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = x;
-    __syncthreads();
+    const int64_t first = lead + chunk * kChunk<T>;
+    const T* p = g + first + threadIdx.x * kVecElems;
+    const T* stop = p + kChunk<T>;
+    float2 sum[2] = {};
+    if (first + kChunk<T> <= n) {
+        Eight<T> v[kVecs<T>];
+#pragma unroll
+        for (int j = 0; j < kVecs<T>; ++j) v[j].template read<KEEP>(p + j * kGradThreads * kVecElems);
+#pragma unroll
+        for (int j = 0; j < kVecs<T>; ++j) add_squares(v[j], sum);
+    } else {
+        const int64_t whole = first + (max(n - first, int64_t(0)) / kVecElems) * kVecElems;
+        stop = g + whole;
+#pragma unroll 2
+        for (const T* q = p; q < stop; q += kGradThreads * kVecElems) {
+            Eight<T> v;
+            v.template read<KEEP>(q);
+            add_squares(v, sum);
+        }
+        if (whole + threadIdx.x < n) total.add1(load1(g + whole + threadIdx.x));
+    }
+    if (chunk == 0 && static_cast<int>(threadIdx.x) < lead && threadIdx.x < n) total.add1(load1(g + threadIdx.x));
+    const float s = __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y));
+    if (Sum::in_range(s)) {
+        total.add(s);
+    } else {
+        const double x = squares_scaled(p, stop);
+        if (x != 0.0) total.add_rare(x);
+    }
+}
+
+// The CTA's sum, to thread 0.
+__device__ __forceinline__ double block_sum(Sum x)
+{
+    __shared__ float2 s[kGradThreads / 32];
+    __shared__ double r[kGradThreads / 32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (int o = 16; o > 0; o /= 2) {
+        const float hi = __shfl_xor_sync(~0u, x.hi, o), lo = __shfl_xor_sync(~0u, x.lo, o);
+        x.add(hi);
+        x.lo = __fadd_rn(x.lo, lo);
+    }
+    if (lane == 0) s[warp] = make_float2(x.hi, x.lo);
+    const bool any = __syncthreads_or(x.any);
+    if (any) {
+        for (int o = 16; o > 0; o /= 2) x.rare += __shfl_xor_sync(~0u, x.rare, o);
+        if (lane == 0) r[warp] = x.rare;
+        __syncthreads();
+    }
     double sum = 0.0;
-    for (int w = 0; w < kGradThreads / 32; ++w) sum += s[w];
-    __syncthreads();
+    if (threadIdx.x == 0) {
+        Sum t;
+        for (int w = 0; w < kGradThreads / 32; ++w) {
+            t.add(s[w].x);
+            t.lo = __fadd_rn(t.lo, s[w].y);
+        }
+        sum = static_cast<double>(t.hi) + static_cast<double>(t.lo);
+        if (any)
+            for (int w = 0; w < kGradThreads / 32; ++w) sum += r[w];
+    }
     return sum;
 }
 
-// The squares of one thread's elements first, first + kGradThreads, ... of a
-// chunk that ends at `last`.
-__device__ double squares(const void* g, bool f32, int64_t first, int64_t last)
-{
-    float sum = 0.0f;
-    for (int64_t i = first; i < last; i += kGradThreads) {
-        const float x = load(g, f32, i);
-        sum = __fmaf_rn(x, x, sum);
-    }
-    if (sum >= 0x1p-70f && sum <= 0x1p126f) return sum;
-    // squares may have left fp32's range: the largest magnitude picks a power of
-    // two that brings all of them, or all that count, back into it
-    uint32_t top = 0;
-    for (int64_t i = first; i < last; i += kGradThreads) top = max(top, __float_as_uint(load(g, f32, i)) & 0x7FFFFFFFu);
-    const int exponent = static_cast<int>(top >> 23) - 127;
-    if (top == 0 || exponent == 128) return sum;
-    const int k = max(-126, min(126, -exponent));
-    const float scale = __int_as_float((127 + k) << 23);
-    sum = 0.0f;
-    for (int64_t i = first; i < last; i += kGradThreads) {
-        const float x = __fmul_rn(load(g, f32, i), scale);
-        sum = __fmaf_rn(x, x, sum);
-    }
-    return ldexp(static_cast<double>(sum), -2 * k);
-}
+// Kernels of one call follow one another closely: the next one's CTAs take the
+// places that this one's leave, and wait until all of its memory is there.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-__global__ void __launch_bounds__(kGradThreads) squares_kernel(const __grid_constant__ GradArgs a)
+template <int ROOM>
+__global__ void __launch_bounds__(kGradThreads, kPerSm) squares_kernel(const __grid_constant__ GradArgs<ROOM> a)
 {
-    __shared__ double s[kGradThreads / 32];
+    let_next_start();
     const int64_t begin = blockIdx.x * a.nchunks / gridDim.x;
     const int64_t end = (blockIdx.x + 1) * a.nchunks / gridDim.x;
-    double sum = 0.0;
-    int t = begin < end ? find(a.start, a.nt, begin) : 0;
-    for (int64_t c = begin; c < end; ++c) {
+    const int64_t keep = end - a.keep;
+    Sum sum;
+    int t = a.at[blockIdx.x];
+    for (int64_t c = begin; c < end;) {
         while (c >= a.start[t + 1]) ++t;
-        const int64_t first = (c - a.start[t]) * kChunk;
-        sum += squares(a.d[t].g, a.f32[t] & 1, first + threadIdx.x, min(first + kChunk, a.d[t].n));
+        const Grad& d = a.d[t];
+        const Kind k = a.kind[t];
+        const int64_t base = a.start[t], stop = min(end, a.start[t + 1]), gone = min(stop, keep);
+        if (k.flags & kF32) {
+            for (; c < gone; ++c) chunk_squares<false>(sum, static_cast<const float*>(d.g), d.n, k.lead, c - base);
+            for (; c < stop; ++c) chunk_squares<true>(sum, static_cast<const float*>(d.g), d.n, k.lead, c - base);
+        } else {
+            for (; c < gone; ++c) chunk_squares<false>(sum, static_cast<const uint16_t*>(d.g), d.n, k.lead, c - base);
+            for (; c < stop; ++c) chunk_squares<true>(sum, static_cast<const uint16_t*>(d.g), d.n, k.lead, c - base);
+        }
     }
-    sum = block_sum(sum, s);
-    if (threadIdx.x == 0) a.parts[a.parts_at + blockIdx.x] = sum;
+    const double x = block_sum(sum);
+    if (threadIdx.x == 0) a.parts[a.parts_at + blockIdx.x] = x;
 }
 
-__device__ double total(const double* parts, int n, double* s)
+// A part over 2^e (e even, that of the largest part: 0 <= result < 4) in fp32,
+// by integer operations on its bits: no double arithmetic.
+__device__ __forceinline__ float scaled(uint64_t x, int e)
 {
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < n; i += kGradThreads) sum += parts[i];
-    return sqrt(block_sum(sum, s));
+    if ((x >> 52 & 0x7FF) == 0x7FF) return x << 12 ? NAN : INFINITY;
+    x += uint64_t(1) << 28;                                // rounded to 23 bits, up at a half
+    const int by = static_cast<int>(x >> 52) - 1023 - e;
+    const float m = __uint_as_float((static_cast<uint32_t>(x >> 29) & 0x7FFFFFu) | 0x3F800000u);
+    return by > -126 ? __fmul_rn(m, __uint_as_float(static_cast<uint32_t>(127 + by) << 23)) : 0.0f;
+}
+
+// The square root of the sum of `n` parts, to all threads of the CTA, to some
+// twelve roundings of fp32.
+__device__ __forceinline__ float norm_of(const double* parts, int n)
+{
+    __shared__ int top[kGradThreads / 32];
+    __shared__ float sums[kGradThreads / 32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint64_t* bits = reinterpret_cast<const uint64_t*>(parts);
+    int e = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kGradThreads) {
+        const int f = static_cast<int>(bits[i] >> 52) & 0x7FF;
+        if (f != 0x7FF) e = max(e, f);
+    }
+    e = __reduce_max_sync(~0u, e);
+    if (lane == 0) top[warp] = e;
+    __syncthreads();
+    for (int w = 0; w < kGradThreads / 32; ++w) e = max(e, top[w]);
+    e = (e - 1023) & ~1;
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kGradThreads) sum = __fadd_rn(sum, scaled(bits[i], e));
+    for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(~0u, sum, o));
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int w = 0; w < kGradThreads / 32; ++w) sum = __fadd_rn(sum, sums[w]);
+    // sqrt(sum) * 2^(e / 2), the power in two steps: that of a subnormal norm is none
+    const int h0 = max(-126, min(127, e / 2)), h1 = max(-126, min(127, e / 2 - h0));
+    return __fmul_rn(__fmul_rn(__fsqrt_rn(sum), __uint_as_float(static_cast<uint32_t>(127 + h0) << 23)),
+                     __uint_as_float(static_cast<uint32_t>(127 + h1) << 23));
 }
 
 __global__ void __launch_bounds__(kGradThreads) norm_kernel(const double* parts, int n, float* norm)
 {
-    __shared__ double s[kGradThreads / 32];
-    const double x = total(parts, n, s);
-    if (threadIdx.x == 0) *norm = static_cast<float>(x);
+    wait_for_previous();
+    const float x = norm_of(parts, n);
+    if (threadIdx.x == 0) *norm = x;
 }
 
-__global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constant__ GradArgs a)
+__device__ __forceinline__ uint32_t bf16_pair(float2 x)
 {
-    __shared__ double s[kGradThreads / 32];
-    const double norm = total(a.parts, a.nparts, s);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = static_cast<float>(norm);
-    const double ratio = a.max_norm / (norm + 1e-6);
-    const float c = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);       // NaN stays NaN
-    const int64_t begin = blockIdx.x * a.nchunks / gridDim.x;
-    const int64_t end = (blockIdx.x + 1) * a.nchunks / gridDim.x;
-    int t = begin < end ? find(a.start, a.nt, begin) : 0;
-    for (int64_t k = begin; k < end; ++k) {
-        while (k >= a.start[t + 1]) ++t;
-        const Grad& d = a.d[t];
-        if (c == 1.0f && d.out == d.g) continue;
-        const int64_t first = (k - a.start[t]) * kChunk, last = min(first + kChunk, d.n);
-        for (int64_t i = first + threadIdx.x; i < last; i += kGradThreads) {
-            const float x = __fmul_rn(load(d.g, a.f32[t] & 1, i), c);
-            if (a.f32[t] & 2) static_cast<float*>(d.out)[i] = x;
-            else static_cast<uint16_t*>(d.out)[i] = float_to_bf16(x);
+    return static_cast<uint32_t>(float_to_bf16(x.x)) | static_cast<uint32_t>(float_to_bf16(x.y)) << 16;
+}
+
+template <typename T>
+__device__ __forceinline__ void write8(const Eight<T>& v, float2 c, uint16_t* p, bool vec)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(__fmul2_rn(v.pair(i), c));
+    if (vec) {
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void write8(const Eight<T>& v, float2 c, float* p, bool vec)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float2 x = __fmul2_rn(v.pair(i), c), y = __fmul2_rn(v.pair(i + 1), c);
+        if (vec) {
+            __stcs(reinterpret_cast<float4*>(p + 2 * i), make_float4(x.x, x.y, y.x, y.y));
+        } else {
+            p[2 * i] = x.x;
+            p[2 * i + 1] = x.y;
+            p[2 * i + 2] = y.x;
+            p[2 * i + 3] = y.y;
         }
     }
+}
+
+template <typename T, typename O>
+__device__ __noinline__ void chunk_clip(const T* g, O* out, int64_t n, int lead, bool vec, int64_t chunk, float c)
+{
+    constexpr int kStep = kGradThreads * kVecElems;
+    const int64_t first = lead + chunk * kChunk<T>;
+    const int64_t at = first + threadIdx.x * kVecElems;
+    if (first + kChunk<T> <= n) {
+        Eight<T> v[kVecs<T>];
+#pragma unroll
+        for (int j = 0; j < kVecs<T>; ++j) v[j].template read<false>(g + at + j * kStep);
+#pragma unroll
+        for (int j = 0; j < kVecs<T>; ++j) write8(v[j], splat(c), out + at + j * kStep, vec);
+    } else {
+        const int64_t whole = first + (max(n - first, int64_t(0)) / kVecElems) * kVecElems;
+#pragma unroll 2
+        for (int64_t i = at; i < whole; i += kStep) {
+            Eight<T> v;
+            v.template read<false>(g + i);
+            write8(v, splat(c), out + i, vec);
+        }
+        if (whole + threadIdx.x < n) store1(out + whole + threadIdx.x, __fmul_rn(load1(g + whole + threadIdx.x), c));
+    }
+    if (chunk == 0 && static_cast<int>(threadIdx.x) < lead && threadIdx.x < n) store1(out + threadIdx.x, __fmul_rn(load1(g + threadIdx.x), c));
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_clip(const T* g, const Grad& d, Kind k, int64_t chunk, float c)
+{
+    const bool vec = k.flags & kOutVec;
+    if (k.flags & kOutF32) chunk_clip(g, static_cast<float*>(d.out), d.n, k.lead, vec, chunk, c);
+    else chunk_clip(g, static_cast<uint16_t*>(d.out), d.n, k.lead, vec, chunk, c);
+}
+
+template <int ROOM>
+__global__ void __launch_bounds__(kGradThreads, kPerSm) clip_kernel(const __grid_constant__ GradArgs<ROOM> a)
+{
+    const int64_t begin = blockIdx.x * a.nchunks / gridDim.x;
+    int64_t c = (blockIdx.x + 1) * a.nchunks / gridDim.x;
+    int t = a.at[blockIdx.x + 1];
+    wait_for_previous();
+    const float norm = norm_of(a.parts, a.nparts);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
+    const float ratio = __fdiv_rn(a.max_norm, __fadd_rn(norm, 1e-6f));
+    const float f = ratio >= 1.0f ? 1.0f : ratio;                          // NaN stays NaN
+    while (c > begin) {
+        while (c <= a.start[t]) --t;
+        const Grad& d = a.d[t];
+        const Kind k = a.kind[t];
+        const int64_t base = a.start[t], stop = max(begin, base);
+        if (f == 1.0f && d.out == d.g) {
+            c = stop;
+        } else if (k.flags & kF32) {
+            while (c > stop) chunk_clip(static_cast<const float*>(d.g), d, k, --c - base, f);
+        } else {
+            while (c > stop) chunk_clip(static_cast<const uint16_t*>(d.g), d, k, --c - base, f);
+        }
+    }
+}
+
+// The kernel after another one of the same call (wait_for_previous).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), int grid, cudaStream_t st, const Args&... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// An entry's place in a launch: its vectors' alignment and its chunks.
+template <int ROOM>
+void add(GradArgs<ROOM>& a, const q8_grad& g)
+{
+    const int size = g.grad_dtype == Q8_F32 ? 4 : 2, out_size = g.out_dtype == Q8_F32 ? 4 : 2;
+    const int lead = static_cast<int>((16 - reinterpret_cast<uintptr_t>(g.grad) % 16) % 16) / size;
+    const bool vec = (reinterpret_cast<uintptr_t>(g.out) + lead * out_size) % 16 == 0;
+    const int chunk = size == 4 ? kChunk<float> : kChunk<uint16_t>;
+    const int n = a.nt++;
+    a.d[n] = Grad{g.grad, g.out, g.numel};
+    a.kind[n] = Kind{static_cast<uint8_t>((size == 4 ? kF32 : 0) | (out_size == 4 ? kOutF32 : 0) | (vec ? kOutVec : 0)),
+                     static_cast<uint8_t>(lead)};
+    a.start[n + 1] = a.start[n] + std::max<int64_t>(1, (g.numel - lead + chunk - 1) / chunk);
+}
+
+template <int ROOM>
+cudaError_t run_grads(const q8_grad* list, int count, bool clip, double max_norm, float* norm, void* workspace, cudaStream_t st)
+{
+    int grid = 0;                              // of both kernels, so that a CTA finds in L2 what it read last
+    cudaError_t e = persistent_grid(reinterpret_cast<const void*>(squares_kernel<ROOM>), kGradThreads, 0, &grid);
+    if (e != cudaSuccess) return e;
+    grid = std::min(grid, kMaxParts);
+    GradArgs<ROOM> a;
+    a.parts = static_cast<double*>(workspace);
+    a.norm = norm;
+    a.max_norm = static_cast<float>(std::isinf(max_norm) ? max_norm : std::min(max_norm, static_cast<double>(FLT_MAX)));
+    a.nparts = 0;
+    int parts = 0;
+    for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
+        bool first = true;
+        for (int i = 0; i < count;) {
+            if (pass == 0 || count > ROOM) {               // the second pass finds a list of one launch as the first left it
+                a.nt = 0;
+                a.start[0] = 0;
+                for (; i < count && a.nt < ROOM; ++i)
+                    if (list[i].numel) add(a, list[i]);
+                a.nchunks = a.start[a.nt];
+            } else {
+                i = count;
+            }
+            if (a.nchunks == 0) continue;
+            const int ctas = static_cast<int>(std::min<int64_t>(grid, a.nchunks));
+            for (int b = 0, t = 0; b <= ctas; ++b) {
+                while (t + 1 < a.nt && b * a.nchunks / ctas >= a.start[t + 1]) ++t;
+                a.at[b] = static_cast<uint16_t>(t);
+            }
+            if (pass == 0) {
+                a.parts_at = parts;
+                a.keep = clip ? kKeepBytes / kChunkBytes / ctas : 0;
+                parts += ctas;
+                squares_kernel<ROOM><<<ctas, kGradThreads, 0, st>>>(a);
+            } else if (first) {
+                if ((e = launch_after(clip_kernel<ROOM>, ctas, st, a)) != cudaSuccess) return e;
+                first = false;
+            } else {
+                clip_kernel<ROOM><<<ctas, kGradThreads, 0, st>>>(a);
+            }
+        }
+        a.nparts = parts;
+    }
+    if (parts == 0) norm_kernel<<<1, kGradThreads, 0, st>>>(a.parts, 0, norm);
+    else if (!clip) e = launch_after(norm_kernel, 1, st, static_cast<const double*>(a.parts), parts, norm);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int ROOM>
+cudaError_t prepare_room()
+{
+    int g = 0;
+    const cudaError_t e = persistent_grid(reinterpret_cast<const void*>(squares_kernel<ROOM>), kGradThreads, 0, &g);
+    return e != cudaSuccess ? e : persistent_grid(reinterpret_cast<const void*>(clip_kernel<ROOM>), kGradThreads, 0, &g);
 }
 
 }  // namespace
@@ -154,12 +502,9 @@ __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constan
 cudaError_t prepare_grads()
 {
     int g = 0;
-    for (const void* k : {reinterpret_cast<const void*>(squares_kernel), reinterpret_cast<const void*>(norm_kernel),
-                          reinterpret_cast<const void*>(clip_kernel)}) {
-        const cudaError_t e = persistent_grid(k, kGradThreads, 0, &g);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    cudaError_t e = persistent_grid(reinterpret_cast<const void*>(norm_kernel), kGradThreads, 0, &g);
+    if (e == cudaSuccess) e = prepare_room<kFewGrads>();
+    return e == cudaSuccess ? prepare_room<kMaxGrads>() : e;
 }
 
 int64_t grads_workspace(int count) { return (static_cast<int64_t>(count) / kMaxGrads + 1) * kMaxParts * 8; }
@@ -167,40 +512,8 @@ int64_t grads_workspace(int count) { return (static_cast<int64_t>(count) / kMaxG
 cudaError_t launch_grads(const q8_grad* list, int count, bool clip, double max_norm, float* norm, void* workspace,
                          cudaStream_t st)
 {
-    int grid = 0;
-    cudaError_t e = persistent_grid(reinterpret_cast<const void*>(squares_kernel), kGradThreads, 0, &grid);
-    if (e != cudaSuccess) return e;
-    grid = std::min(grid, kMaxParts);
-    std::unique_ptr<GradArgs> a(new GradArgs());
-    a->parts = static_cast<double*>(workspace);
-    a->norm = norm;
-    a->max_norm = max_norm;
-    int parts = 0;
-    for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
-        int at = 0;
-        for (int i = 0; i < count;) {
-            a->nt = 0;
-            a->start[0] = 0;
-            for (; i < count && a->nt < kMaxGrads; ++i) {
-                if (list[i].numel == 0) continue;
-                const int n = a->nt++;
-                a->d[n] = Grad{list[i].grad, list[i].out, list[i].numel};
-                a->f32[n] = static_cast<uint8_t>((list[i].grad_dtype == Q8_F32 ? 1 : 0) | (list[i].out_dtype == Q8_F32 ? 2 : 0));
-                a->start[n + 1] = a->start[n] + (list[i].numel + kChunk - 1) / kChunk;
-            }
-            a->nchunks = a->start[a->nt];
-            if (a->nchunks == 0) continue;
-            const int ctas = static_cast<int>(std::min<int64_t>(grid, a->nchunks));
-            a->parts_at = at;
-            at += ctas;
-            a->nparts = parts;
-            if (pass == 0) squares_kernel<<<ctas, kGradThreads, 0, st>>>(*a);
-            else clip_kernel<<<ctas, kGradThreads, 0, st>>>(*a);
-        }
-        parts = at;
-    }
-    if (!clip || parts == 0) norm_kernel<<<1, kGradThreads, 0, st>>>(a->parts, parts, norm);
-    return cudaGetLastError();
+    return count <= kFewGrads ? run_grads<kFewGrads>(list, count, clip, max_norm, norm, workspace, st)
+                              : run_grads<kMaxGrads>(list, count, clip, max_norm, norm, workspace, st);
 }
 
 }  // namespace q8

@@ -252,9 +252,9 @@ int q8_embedding_backward(const q8_embedding* e, const void* dout, int64_t dout_
  *   norm = sqrt(sum over i, j of g_ij^2)
  *   c = min(1, max_norm / (norm + 1e-6)),  out_ij = c * g_ij.
  * Squares are summed in fp32 over at most 128 elements, scaled by a power of
- * two where they would leave fp32's range, and then in double, so that no norm
- * below 2^128 overflows and none above 2^-140 is lost; `norm` is rounded once,
- * and so is c.  With an infinite gradient the norm is infinite and c is 0
+ * two where they would leave fp32's range, and from there in pairs of fp32 (or
+ * double): no norm below 2^128 overflows, none is lost, and beyond the 128
+ * terms' roundings norm and c carry less than 16 roundings of fp32 each.  With an infinite gradient the norm is infinite and c is 0
  * (infinite elements then give NaN); with NaN both are NaN and all results are.
  * grad and out are contiguous, on their elements' own alignment; out may be
  * grad itself where both have one type, and out_dtype may differ from
