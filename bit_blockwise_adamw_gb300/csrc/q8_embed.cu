@@ -9,17 +9,18 @@
 //  1. order_kernel.  One cluster of eight CTAs sorts the tokens by their id
 //     (stable, so that a row's tokens keep their order: least significant digit
 //     first, up to nine bits a pass, counts exchanged through the cluster's
-//     shared memory), while all other CTAs write the zeros of the table's rows
-//     that no token has.
-//  2. sum_kernel.  The sorted tokens are cut into pieces of kPiece; a group of
+//     shared memory), while all other CTAs write zeros into the first of the
+//     table's rows that no token has.
+//  2. sum_kernel.  The sorted tokens are cut into pieces of 8 or 32; a group of
 //     warps adds up a piece's rows for its columns, in fp32 registers, and
-//     writes a table row whenever the id changes.  An id of at most kPiece
-//     tokens belongs to the piece that it begins in; longer ones (padding,
+//     writes a table row whenever the id changes.  An id of no more tokens than
+//     a piece has belongs to the piece that it begins in; longer ones (padding,
 //     frequent words) are split at the pieces' ends, their parts left in the
-//     workspace in fp32.
+//     workspace in fp32.  Further CTAs write the other zeros.
 //  3. join_kernel adds up these parts, in their order.
 // No result depends on which CTA comes first.
 #include <algorithm>
+#include <limits>
 #include <map>
 #include <mutex>
 
@@ -35,7 +36,6 @@ namespace {
 constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_float(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = float_to_bf16(x); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kRowThreads) lookup_odd_kernel(q8_embedding e,
 
 // ---------------------------------------------------------------------- gradient
 
-constexpr int kPiece = 32;
+constexpr int kFewParts = 32;
 constexpr int kCluster = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -137,18 +137,35 @@ constexpr int kMapBits = kSortShared * 8;      // rows that a filling CTA's bitm
 struct Room {
     uint64_t* sorted;          // [tokens]: id << 32 | token, ids outside the table as vocab
     uint64_t* other;           // the sort's second buffer
-    int32_t* count;            // ids whose parts are to be joined
-    int32_t* list;             // [pieces]: the piece that each of them begins in
+    int32_t* count;            // [2]: ids whose parts are to be joined, of few parts and of many
+    int2* list;                // [2][pieces]: the piece that each of them begins in, and its parts
     float* parts;              // [pieces][2][columns]: of an id from before the piece; of one that goes on behind it
     int64_t columns;           // dim, to whole vectors
+    int64_t pieces;
+    int32_t piece;             // tokens of one
     int64_t bytes;
 };
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+// Threads that share a piece's columns, eight columns each.
+int group_of(const q8_embedding& e)
+{
+    int group = 32;
+    while (group < kRowThreads && group * int64_t(8) < e.dim) group *= 2;
+    return group;
+}
+
+// Pieces of 32, or of 8 where 32 would leave half of the GPU's 152 SMs with
+// less than four groups of 256 threads: a piece's rows are added one after the
+// other, and few tokens then wait for that (times beside launch_embed_backward).
+constexpr int64_t kFewThreads = 152 / 2 * 4 * 256;
+
 Room room_of(const q8_embedding& e, void* workspace)
 {
-    const int64_t pieces = round_up(e.tokens, kPiece) / kPiece;
+    const int64_t group = group_of(e), threads = round_up(e.tokens, 32) / 32 * group * ((e.dim + group * 8 - 1) / (group * 8));
+    const int piece = threads < kFewThreads ? 8 : 32;
+    const int64_t pieces = round_up(e.tokens, piece) / piece;
     char* p = static_cast<char*>(workspace);
     int64_t at = 0;
     const auto take = [&](int64_t bytes) {
@@ -157,11 +174,13 @@ Room room_of(const q8_embedding& e, void* workspace)
         return q;
     };
     Room r{};
+    r.piece = piece;
+    r.pieces = pieces;
     r.columns = round_up(e.dim, 8);
     r.sorted = reinterpret_cast<uint64_t*>(take(e.tokens * 8));
     r.other = reinterpret_cast<uint64_t*>(take(e.tokens * 8));
-    r.count = reinterpret_cast<int32_t*>(take(4));
-    r.list = reinterpret_cast<int32_t*>(take(pieces * 4));
+    r.count = reinterpret_cast<int32_t*>(take(8));
+    r.list = reinterpret_cast<int2*>(take(2 * pieces * 8));
     r.parts = reinterpret_cast<float*>(take(pieces * 2 * r.columns * 4));
     r.bytes = at;
     return r;
@@ -172,7 +191,7 @@ struct OrderArgs {
     Room r;
     uint16_t* dtable;
     int32_t passes, digit;     // of the sort: passes, bits of each
-    int32_t fill;              // 0: nothing; 1: all rows; 2: rows that no token has
+    int64_t fill;              // the table's rows [0, fill) get their zeros here
 };
 
 __device__ __forceinline__ uint32_t cluster_read(const uint32_t* p, uint32_t rank)
@@ -182,44 +201,106 @@ __device__ __forceinline__ uint32_t cluster_read(const uint32_t* p, uint32_t ran
     return v;
 }
 
+// The warp's lanes that have this lane's digit (of `bits` bits), among those that
+// are on: a ballot for each bit.  __match_any_sync took four times as long.
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, bool on, int bits)
+{
+    uint32_t same = __ballot_sync(~0u, on);
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {
+        if (b >= bits) break;
+        const uint32_t set = __ballot_sync(~0u, d >> b & 1);
+        same &= d >> b & 1 ? set : ~set;
+    }
+    return same;
+}
+
 // One CTA's part of the sort: the tokens [lo, hi) of each pass's order.
 __device__ void sort_tokens(const OrderArgs& a, uint32_t (*counts)[kBins])
 {
-    __shared__ uint32_t hist[kBins], base[kBins], sums[kSortWarps];
+    __shared__ uint32_t hist[kBins], sums[kSortWarps];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const uint32_t rank = cluster_rank();
     const int64_t T = a.e.tokens;
     const int64_t lo = T * rank / kCluster, hi = T * (rank + 1) / kCluster;
     const int items = static_cast<int>(max(int64_t(1), min(int64_t(kItems), (hi - lo + kSortThreads - 1) / kSortThreads)));
     const int bins = 1 << a.digit;
-    if (rank == 0 && tid == 0) *a.r.count = 0;
+    if (rank == 0 && tid < 2) a.r.count[tid] = 0;
+    const int64_t tile = static_cast<int64_t>(kSortThreads) * items;
+    const bool single = hi - lo <= tile;       // its tokens then stay in registers from counting to placing
+    uint64_t x[kItems];
+    uint32_t place[kItems];
     for (int pass = 0; pass < a.passes; ++pass) {
         const uint64_t* from = (a.passes - pass) % 2 ? a.r.other : a.r.sorted;
         uint64_t* to = (a.passes - pass) % 2 ? a.r.sorted : a.r.other;
         const int shift = 32 + pass * a.digit;
-        const auto token = [&](int64_t i) {
-            if (pass > 0) return __ldcg(reinterpret_cast<const unsigned long long*>(from) + i);
-            const int64_t id = a.e.ids[i];
-            const uint32_t key = static_cast<uint32_t>(id >= 0 && id < a.e.vocab ? id : a.e.vocab);
-            return static_cast<unsigned long long>(key) << 32 | static_cast<uint32_t>(i);
+        const auto load = [&](int64_t at) {
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                const int64_t i = at + (warp * items + j) * 32 + lane;
+                if (j >= items || i >= hi) continue;
+                if (pass > 0) {
+                    x[j] = __ldcg(reinterpret_cast<const unsigned long long*>(from) + i);
+                } else {
+                    const int64_t id = a.e.ids[i];
+                    const uint32_t key = static_cast<uint32_t>(id >= 0 && id < a.e.vocab ? id : a.e.vocab);
+                    x[j] = static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(i);
+                }
+            }
         };
-        for (int d = tid; d < bins; d += kSortThreads) hist[d] = 0;
-        __syncthreads();
-        for (int64_t i0 = lo + warp * 32; i0 < hi; i0 += kSortThreads) {
-            const bool on = i0 + lane < hi;
-            const uint32_t d = on ? static_cast<uint32_t>(token(i0 + lane) >> shift) & (bins - 1) : ~0u;
-            const uint32_t same = __match_any_sync(~0u, d);
-            if (on && lane == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
+        const auto digit = [&](int64_t at, int j) {
+            return at + (warp * items + j) * 32 + lane < hi ? static_cast<uint32_t>(x[j] >> shift) & (bins - 1) : ~0u;
+        };
+        // each token's place among its warp's of the same digit, and the warp's counts
+        const auto rank_tile = [&](int64_t at) {
+            __syncwarp();                      // its lanes have read their places of the tile before
+            for (int d = lane; d < bins; d += 32) counts[warp][d] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                if (j >= items) break;
+                const uint32_t d = digit(at, j), same = same_digit(d, d != ~0u, a.digit);
+                const uint32_t seen = d != ~0u ? counts[warp][d] : 0;
+                place[j] = seen + __popc(same & ((1u << lane) - 1));
+                __syncwarp();
+                if (d != ~0u && lane == __ffs(same) - 1) counts[warp][d] = seen + __popc(same);
+                __syncwarp();
+            }
+            __syncthreads();
+        };
+        if (single) {
+            load(lo);
+            rank_tile(lo);
+            if (tid < bins) {
+                uint32_t n = 0;
+#pragma unroll 8
+                for (int w = 0; w < kSortWarps; ++w) n += counts[w][tid];
+                hist[tid] = n;
+            }
+        } else {
+            for (int d = tid; d < bins; d += kSortThreads) hist[d] = 0;
+            __syncthreads();
+            for (int64_t at = lo; at < hi; at += tile) {
+                load(at);
+#pragma unroll
+                for (int j = 0; j < kItems; ++j) {
+                    if (j >= items) break;
+                    const uint32_t d = digit(at, j), same = same_digit(d, d != ~0u, a.digit);
+                    if (d != ~0u && lane == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
+                }
+            }
         }
         cluster_sync();
         // a digit's first place: all smaller digits, and its own in the CTAs before
         uint32_t all = 0, before = 0;
-        if (tid < bins)
+        if (tid < bins) {
+#pragma unroll
             for (uint32_t c = 0; c < kCluster; ++c) {
                 const uint32_t h = cluster_read(&hist[tid], c);
                 all += h;
                 before += c < rank ? h : 0;
             }
+        }
         uint32_t sum = all;
         for (int o = 1; o < 32; o *= 2) {
             const uint32_t s = __shfl_up_sync(~0u, sum, o);
@@ -227,47 +308,28 @@ __device__ void sort_tokens(const OrderArgs& a, uint32_t (*counts)[kBins])
         }
         if (lane == 31) sums[warp] = sum;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) sum += sums[w];
-        if (tid < bins) base[tid] = sum - all + before;
-        for (int64_t tile = lo; tile < hi; tile += kSortThreads * items) {
-            __syncwarp();                      // its lanes have read their places of the tile before
-            for (int d = lane; d < bins; d += 32) counts[warp][d] = 0;
-            __syncwarp();
-            uint64_t x[kItems];
-            uint32_t place[kItems];
-#pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-                const int64_t i = tile + (warp * items + j) * 32 + lane;
-                x[j] = j < items && i < hi ? token(i) : ~uint64_t(0);
+        if (tid < bins)
+            for (int w = 0; w < warp; ++w) sum += sums[w];
+        uint32_t base = sum - all + before;    // of digit tid
+        for (int64_t at = lo; at < hi; at += tile) {
+            if (!single) {
+                load(at);
+                rank_tile(at);
             }
-#pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-                if (j >= items) break;
-                const bool on = tile + (warp * items + j) * 32 + lane < hi;
-                const uint32_t d = on ? static_cast<uint32_t>(x[j] >> shift) & (bins - 1) : ~0u;
-                const uint32_t same = __match_any_sync(~0u, d);
-                const uint32_t seen = on ? counts[warp][d] : 0;
-                place[j] = seen + __popc(same & ((1u << lane) - 1));
-                __syncwarp();
-                if (on && lane == __ffs(same) - 1) counts[warp][d] = seen + __popc(same);
-                __syncwarp();
-            }
-            __syncthreads();
             if (tid < bins) {
-                uint32_t at = base[tid];
+#pragma unroll 8
                 for (int w = 0; w < kSortWarps; ++w) {
                     const uint32_t n = counts[w][tid];
-                    counts[w][tid] = at;
-                    at += n;
+                    counts[w][tid] = base;
+                    base += n;
                 }
-                base[tid] = at;
             }
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < kItems; ++j) {
                 if (j >= items) break;
-                if (tile + (warp * items + j) * 32 + lane < hi)
-                    to[counts[warp][static_cast<uint32_t>(x[j] >> shift) & (bins - 1)] + place[j]] = x[j];
+                const uint32_t d = digit(at, j);
+                if (d != ~0u) to[counts[warp][d] + place[j]] = x[j];
             }
         }
         cluster_sync();                        // what all CTAs wrote is there, and their counts are read
@@ -286,17 +348,11 @@ __device__ __forceinline__ void zero_run(uint16_t* p, int64_t n, int lane)
     if (lead + vecs * 8 + lane < n) p[lead + vecs * 8 + lane] = 0;
 }
 
-// One CTA's part of the zeros.
+// One CTA's part of the zeros: the table's rows [begin, end) that no token has.
 __device__ void fill_rows(const OrderArgs& a, uint32_t* map, int64_t cta, int64_t ctas)
 {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t begin = a.e.vocab * cta / ctas, end = a.e.vocab * (cta + 1) / ctas;
-    if (a.fill == 1) {                         // in runs of 8192 elements, a warp each
-        const int64_t n = (end - begin) * a.e.dim;
-        for (int64_t i = warp * int64_t(8192); i < n; i += kSortWarps * int64_t(8192))
-            zero_run(a.dtable + begin * a.e.dim + i, min(int64_t(8192), n - i), lane);
-        return;
-    }
+    const int64_t begin = a.fill * cta / ctas, end = a.fill * (cta + 1) / ctas;
     for (int64_t first = begin; first < end; first += kMapBits) {
         const int64_t rows = min(int64_t(kMapBits), end - first);
         for (int64_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) map[i] = 0;
@@ -304,11 +360,13 @@ __device__ void fill_rows(const OrderArgs& a, uint32_t* map, int64_t cta, int64_
 #pragma unroll 4
         for (int64_t t = threadIdx.x; t < a.e.tokens; t += kSortThreads) {
             const uint64_t r = static_cast<uint64_t>(a.e.ids[t]) - static_cast<uint64_t>(first);
-            if (r < static_cast<uint64_t>(rows)) atomicOr(&map[r / 32], 1u << (r % 32));
+            // seen before by most tokens of a frequent id: they would wait for one another's atomics
+            if (r < static_cast<uint64_t>(rows) && !(static_cast<volatile uint32_t*>(map)[r / 32] >> (r % 32) & 1)) atomicOr(&map[r / 32], 1u << (r % 32));
         }
         __syncthreads();
-        for (int64_t r = warp; r < rows; r += kSortWarps)
+        for (int64_t r = warp; r < rows; r += kSortWarps) {
             if (!(map[r / 32] >> (r % 32) & 1)) zero_run(a.dtable + (first + r) * a.e.dim, a.e.dim, lane);
+        }
         __syncthreads();
     }
 }
@@ -330,218 +388,313 @@ struct SumArgs {
     const void* dout;
     int64_t stride;
     uint16_t* dtable;
+    int64_t filled, fill_rows; // the table's rows from `filled` on get their zeros here, so many to a CTA
+    int64_t sums;              // CTAs that add up; the others write zeros
     int32_t accumulate;
-    int32_t group;             // threads that share a piece's columns
+    int32_t group, tiles;      // threads that share a piece's columns, and tiles of 8 * group columns
 };
 
 __device__ __forceinline__ uint32_t key_of(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
-// How an id lies across the start p of a piece (p is not the first): `before`
-// of its tokens come before p and `from` from p on, each counted to kPiece.
-struct Cut {
-    uint32_t key;
-    int before, from;
-
-    __device__ __forceinline__ bool crosses() const { return before > 0; }
-    __device__ __forceinline__ bool is_long() const { return before + from > kPiece; }
-};
-
-__device__ __forceinline__ Cut cut_at(const uint64_t* sorted, int64_t T, int64_t p, int lane)
-{
-    static_assert(kPiece == 32, "a lane for each token");
-    Cut c;
-    c.key = key_of(__ldcg(reinterpret_cast<const unsigned long long*>(sorted) + p));
-    const uint32_t back = p - 1 - lane >= 0 ? key_of(__ldcg(reinterpret_cast<const unsigned long long*>(sorted) + p - 1 - lane)) : ~0u;
-    const uint32_t forth = p + lane < T ? key_of(__ldcg(reinterpret_cast<const unsigned long long*>(sorted) + p + lane)) : ~0u;
-    const uint32_t b = ~__ballot_sync(~0u, back == c.key), f = ~__ballot_sync(~0u, forth == c.key);
-    c.before = b ? __ffs(b) - 1 : 32;
-    c.from = f ? __ffs(f) - 1 : 32;
-    return c;
-}
-
-// A thread's eight columns: VEC, contiguous; else every step-th.  What was read
-// of a row stays as it lies in memory until it is added.
-template <bool VEC>
+// A thread's eight columns: VEC, contiguous; else every step-th, of bf16 in
+// pairs.  Rows on their way wait in the thread's own slots of shared memory (no
+// other thread reads them), which hold more of them in flight than registers
+// would.
+template <typename T, bool VEC>
 struct Columns {
+    static constexpr int kBytes = VEC ? 8 * sizeof(T) : 32;        // of a slot
     int64_t first, dim;
     int step;
 
-    template <typename T>
-    struct Raw {
-        uint4 w[VEC ? sizeof(T) / 2 : 1];
-        T x[VEC ? 1 : 8];
-    };
+    __device__ __forceinline__ int64_t column(int j) const
+    {
+        if constexpr (VEC) return first + j;
+        else if constexpr (sizeof(T) == 4) return first + static_cast<int64_t>(j) * step;
+        else return first + static_cast<int64_t>(j / 2) * 2 * step + j % 2;
+    }
+    static __device__ __forceinline__ uint32_t word(uint4* slot, int j)
+    {
+        return smem_addr(reinterpret_cast<uint32_t*>(slot) + (j / 4) * (kRowThreads * 4) + j % 4);
+    }
+    static __device__ __forceinline__ bool off4(const T* row) { return reinterpret_cast<uintptr_t>(row) % 4 != 0; }
 
-    template <typename T>
-    __device__ __forceinline__ void read(Raw<T>& r, const T* row) const
+    // slot: this thread's, kRowThreads vectors apart.  edge: the row is the first
+    // or the last of its matrix, and the words that its pairs lie in may reach
+    // past it.
+    __device__ __forceinline__ void fetch(uint4* slot, const T* row, bool edge) const
     {
         if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(row + first)[i];
-        } else {
+            for (int i = 0; i < kBytes / 16; ++i)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(slot + i * kRowThreads)),
+                             "l"(reinterpret_cast<const uint4*>(row + first) + i) : "memory");
+        } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r.x[j] = first + j * step < dim ? row[first + j * step] : T(0);
-        }
-    }
-    template <typename T>
-    __device__ __forceinline__ static float2 pair(const Raw<T>& r, int k)
-    {
-        if constexpr (!VEC) {
-            return make_float2(load1(&r.x[2 * k]), load1(&r.x[2 * k + 1]));
-        } else if constexpr (sizeof(T) == 2) {
-            return bf16x2(k == 0 ? r.w[0].x : k == 1 ? r.w[0].y : k == 2 ? r.w[0].z : r.w[0].w);
+            for (int j = 0; j < 8; ++j)
+                if (column(j) < dim)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(word(slot, j)), "l"(row + column(j)) : "memory");
+        } else if (edge) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t c = column(2 * k);
+                x[k] = (c < dim ? row[c] : 0) | static_cast<uint32_t>(c + 1 < dim ? row[c + 1] : 0) << 16;
+            }
+            const bool off = off4(row);        // as copies would have brought it
+            slot[0] = off ? make_uint4(x[0] << 16, x[1] << 16, x[2] << 16, x[3] << 16) : make_uint4(x[0], x[1], x[2], x[3]);
+            if (off) slot[kRowThreads] = make_uint4(x[0] >> 16, x[1] >> 16, x[2] >> 16, x[3] >> 16);
         } else {
-            const uint4& v = r.w[k / 2];
-            return k % 2 ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+            // a pair off 4 bytes lies in two words
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(row) & ~uintptr_t(3));
+            const bool off = off4(row);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (column(2 * k) < dim) {
+                    const uint32_t* p = words + column(2 * k) / 2;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(word(slot, k)), "l"(p) : "memory");
+                    if (off) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(word(slot, 4 + k)), "l"(p + 1) : "memory");
+                }
         }
     }
-    template <typename T>
-    __device__ __forceinline__ void write(T* row, const Eight& v) const
+    // What was fetched, added to sum.
+    __device__ __forceinline__ void add(Eight& sum, const uint4* slot, const T* row) const
+    {
+        const uint4 u = slot[0];
+        if constexpr (sizeof(T) == 2) {
+            uint32_t x[4] = {u.x, u.y, u.z, u.w};
+            if constexpr (!VEC) {
+                if (off4(row)) {
+                    const uint4 w = slot[kRowThreads];
+                    const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = __byte_perm(x[k], y[k], 0x5432);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum.x[k] = __fadd2_rn(sum.x[k], bf16x2(x[k]));
+        } else {
+            const uint4 w = slot[kRowThreads];
+            const uint32_t x[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                sum.x[k] = __fadd2_rn(sum.x[k], make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])));
+        }
+    }
+    template <typename U>
+    __device__ __forceinline__ Eight read(const U* row) const
+    {
+        if constexpr (VEC) {
+            const uint4 w = *reinterpret_cast<const uint4*>(row + first);
+            return Eight{{bf16x2(w.x), bf16x2(w.y), bf16x2(w.z), bf16x2(w.w)}};
+        } else {
+            Eight v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v.x[k] = make_float2(column(2 * k) < dim ? load1(row + column(2 * k)) : 0.0f,
+                                     column(2 * k + 1) < dim ? load1(row + column(2 * k + 1)) : 0.0f);
+            return v;
+        }
+    }
+    template <typename U>
+    __device__ __forceinline__ void write(U* row, const Eight& v) const
     {
         if constexpr (VEC) {
             write8(row + first, v);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (first + j * step < dim) store1(row + first + j * step, j % 2 ? v.x[j / 2].y : v.x[j / 2].x);
+                if (column(j) < dim) store1(row + column(j), j % 2 ? v.x[j / 2].y : v.x[j / 2].x);
         }
+    }
+    // scale * sum, or with accumulate that added to what the row holds.
+    __device__ __forceinline__ void write_scaled(uint16_t* row, Eight sum, float scale, bool accumulate) const
+    {
+        if (accumulate) {
+            const Eight old = read(row);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum.x[k] = __ffma2_rn(sum.x[k], splat(scale), old.x[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum.x[k] = __fmul2_rn(sum.x[k], splat(scale));
+        }
+        write(row, sum);
     }
 };
 
-// scale * sum, or with accumulate that added to what the row holds.
-template <bool VEC>
-__device__ __forceinline__ void write_row(const Columns<VEC>& c, uint16_t* row, Eight sum, float scale, bool accumulate)
+template <typename T, bool VEC>
+constexpr int kAhead = 512 / Columns<T, VEC>::kBytes / 2;          // rows in flight: 256 bytes a thread, 64 KB a CTA
+template <typename T, bool VEC>
+constexpr int kSumShared = kAhead<T, VEC> * Columns<T, VEC>::kBytes * kRowThreads;
+
+__device__ __forceinline__ uint64_t entry_at(const uint64_t* sorted, int64_t i, int64_t n, uint64_t none)
 {
-    if (accumulate) {
-        typename Columns<VEC>::template Raw<uint16_t> old;
-        c.read(old, static_cast<const uint16_t*>(row));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum.x[k] = __ffma2_rn(sum.x[k], splat(scale), c.pair(old, k));
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum.x[k] = __fmul2_rn(sum.x[k], splat(scale));
+    return i >= 0 && i < n ? __ldcg(reinterpret_cast<const unsigned long long*>(sorted) + i) : none;
+}
+
+// Zeros of one CTA's rows [begin, end), those that no token has.
+__device__ void fill_absent(const SumArgs& a, int64_t begin, int64_t end)
+{
+    __shared__ uint32_t present[kRowThreads / 32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (int64_t first = begin; first < end; first += kRowThreads) {
+        const int64_t row = first + threadIdx.x;
+        int64_t lo = 0, hi = row < end ? a.e.tokens : 0;   // the first token whose id is not below the row
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (key_of(a.r.sorted[mid]) < row) lo = mid + 1; else hi = mid;
+        }
+        const uint32_t some = __ballot_sync(~0u, row < end && lo < a.e.tokens && key_of(a.r.sorted[lo]) == row);
+        __syncthreads();
+        if (lane == 0) present[warp] = some;
+        __syncthreads();
+        const int rows = static_cast<int>(min(int64_t(kRowThreads), end - first));
+        for (int r = warp; r < rows; r += kRowThreads / 32)
+            if (!(present[r / 32] >> (r % 32) & 1)) zero_run(a.dtable + (first + r) * a.e.dim, a.e.dim, lane);
     }
-    c.write(row, sum);
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) sum_kernel(const __grid_constant__ SumArgs a)
+__global__ void __launch_bounds__(kRowThreads, 3) sum_kernel(const __grid_constant__ SumArgs a)
 {
-    constexpr int kAhead = sizeof(T) == 2 && VEC ? 8 : 4;  // rows in flight: 32 registers
+    constexpr int kRing = kAhead<T, VEC>;
+    constexpr int kVecs = Columns<T, VEC>::kBytes / 16;
+    constexpr int kStep = 4;                               // rows that are waited for together
+    static_assert(kRing % kStep == 0, "the ring holds whole steps");
+    extern __shared__ __align__(16) uint4 ring[];          // [kRing][kVecs][kRowThreads]
     let_next_start();
     wait_for_previous();
+    if (blockIdx.x >= a.sums) {
+        const int64_t begin = a.filled + (blockIdx.x - a.sums) * a.fill_rows;
+        fill_absent(a, begin, min(a.e.vocab, begin + a.fill_rows));
+        return;
+    }
     const int lane = threadIdx.x % 32;
-    const int64_t N = a.e.tokens, pieces = (N + kPiece - 1) / kPiece;
-    const int64_t piece = static_cast<int64_t>(blockIdx.x) * (kRowThreads / a.group) + threadIdx.x / a.group;
-    if (piece >= pieces) return;
-    const uint64_t* sorted = a.r.sorted;
-    const int64_t p0 = piece * kPiece, p1 = min(N, p0 + kPiece);
-    int64_t begin = p0, end = p1;
-    bool from_before = false, goes_on = false;             // parts of a long id
-    if (p0 > 0) {
-        const Cut c = cut_at(sorted, N, p0, lane);
-        from_before = c.crosses() && c.is_long();
-        if (c.crosses() && !from_before) begin += c.from;
-    }
-    if (p1 < N) {
-        const Cut c = cut_at(sorted, N, p1, lane);
-        goes_on = c.crosses() && c.is_long() && c.key < a.e.vocab;
-        if (c.crosses() && !c.is_long()) end += c.from;
-    }
-    // the piece's tokens (at most 63), one or two to a lane
-    const uint64_t none = static_cast<uint64_t>(a.e.vocab) << 32;
-    const uint64_t e0 = begin + lane < end ? __ldcg(reinterpret_cast<const unsigned long long*>(sorted) + begin + lane) : none;
-    const uint64_t e1 = begin + 32 + lane < end ? __ldcg(reinterpret_cast<const unsigned long long*>(sorted) + begin + 32 + lane) : none;
+    const int64_t N = a.e.tokens;
+    const int P = a.r.piece;
+    const int64_t piece = static_cast<int64_t>(blockIdx.x / a.tiles) * (kRowThreads / a.group) + threadIdx.x / a.group;
+    if (piece >= a.r.pieces) return;
+    // the piece's tokens, those behind it (an id goes on for at most P - 1 of
+    // them) and the ids before it, one to a lane
     const uint32_t vocab = static_cast<uint32_t>(a.e.vocab);
-    const int count = __popc(__ballot_sync(~0u, key_of(e0) < vocab)) + __popc(__ballot_sync(~0u, key_of(e1) < vocab));
-    if (count == 0) return;                                // tokens outside the table come last
-    const auto entry = [&](int i) { return __shfl_sync(~0u, i < 32 ? e0 : e1, i % 32); };
-    const uint32_t first_key = key_of(entry(0)), last_key = key_of(entry(count - 1));
+    const uint64_t none = ~uint64_t(0);
+    const int64_t p0 = piece * P;
+    const uint64_t here = entry_at(a.r.sorted, lane < P ? p0 + lane : N, N, none);
+    const uint64_t behind = entry_at(a.r.sorted, lane < P ? p0 + P + lane : N, N, none);
+    const uint32_t before = key_of(entry_at(a.r.sorted, lane < P ? p0 - 1 - lane : N, N, none));
+    const uint32_t first_here = __shfl_sync(~0u, key_of(here), 0), first_behind = __shfl_sync(~0u, key_of(behind), 0);
+    // an id across the piece's start or end: its tokens on either side, each counted to P
+    const auto ones = [](uint32_t m) { return ~m ? __ffs(~m) - 1 : 32; };
+    const int back0 = ones(__ballot_sync(~0u, before == first_here)), on0 = ones(__ballot_sync(~0u, key_of(here) == first_here));
+    const int back1 = __clz(~(__ballot_sync(~0u, key_of(here) == first_behind) << (32 - P)));
+    const int on1 = ones(__ballot_sync(~0u, key_of(behind) == first_behind));
+    const bool from_before = back0 > 0 && back0 + on0 > P;                             // parts of a long id
+    const bool goes_on = first_behind < vocab && back1 > 0 && back1 + on1 > P;
+    const int skip = back0 > 0 && !from_before ? on0 : 0;
+    const int stop = first_behind < vocab && back1 > 0 && !goes_on ? P + on1 : P;
+    const int known = __popc(__ballot_sync(~0u, key_of(here) < vocab)) + __popc(__ballot_sync(~0u, key_of(behind) < vocab));
+    const int count = min(stop, known) - skip;             // ids outside the table come last
+    if (count <= 0) return;
+    const auto key_at = [&](int i) { return __shfl_sync(~0u, i + skip < P ? key_of(here) : key_of(behind), i + skip < P ? i + skip : i + skip - P); };
+    const auto token_at = [&](int i) {
+        return __shfl_sync(~0u, static_cast<uint32_t>(i + skip < P ? here : behind), i + skip < P ? i + skip : i + skip - P);
+    };
+    // bit i: the id of token i (from skip on) ends with it
+    const uint32_t after = __shfl_down_sync(~0u, key_of(here), 1), after2 = __shfl_down_sync(~0u, key_of(behind), 1);
+    const uint32_t m0 = __ballot_sync(~0u, lane < P && key_of(here) != (lane == P - 1 ? first_behind : after));
+    const uint32_t m1 = __ballot_sync(~0u, lane < P && key_of(behind) != after2);
+    const uint64_t ends = ((m0 | static_cast<uint64_t>(m1) << P) >> skip) | uint64_t(1) << (count - 1);
+    const uint32_t first_key = key_at(0), last_key = key_at(count - 1);
     const T* dout = static_cast<const T*>(a.dout);
-    const int64_t width = 8 * static_cast<int64_t>(a.group);
-    for (int64_t c0 = blockIdx.y * width; c0 < a.e.dim; c0 += gridDim.y * width) {
-        const int tid = threadIdx.x % a.group;
-        const Columns<VEC> cols{VEC ? c0 + tid * 8 : c0 + tid, a.e.dim, a.group};
-        const bool on = cols.first < a.e.dim;
-        Eight sum{};
-        uint32_t key = first_key;
-        const auto finish = [&](bool last) {               // the sum of `key` is complete, as far as this piece goes
-            if (!on) return;
-            if (key == first_key && from_before) cols.write(a.r.parts + (piece * 2) * a.r.columns, sum);
-            else if (last && key == last_key && goes_on) cols.write(a.r.parts + (piece * 2 + 1) * a.r.columns, sum);
-            else write_row(cols, a.dtable + static_cast<int64_t>(key) * a.e.dim, sum, a.e.scale, a.accumulate);
-        };
-        for (int i = 0; i < count; i += kAhead) {
-            typename Columns<VEC>::template Raw<T> v[kAhead];
-            uint32_t keys[kAhead];
+    uint4* mine = ring + threadIdx.x;
+    const int tid = threadIdx.x % a.group;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x % a.tiles) * 8 * a.group;
+    const Columns<T, VEC> cols{c0 + tid * (VEC ? 8 : sizeof(T) == 2 ? 2 : 1), a.e.dim, a.group};
+    const bool on = cols.first < a.e.dim;
+    const auto fetch = [&](int i) {                        // kStep rows from i on, one group of copies, be it empty
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const uint64_t x = entry(min(i + j, count - 1));
-                keys[j] = key_of(x);
-                if (on && i + j < count) cols.read(v[j], dout + static_cast<int64_t>(static_cast<uint32_t>(x)) * a.stride);
+        for (int j = 0; j < kStep; ++j)
+            if (i + j < count) {
+                const uint32_t t = token_at(i + j);
+                if (on) cols.fetch(mine + (i % kRing + j) * (kVecs * kRowThreads), dout + static_cast<int64_t>(t) * a.stride, t == 0 || t == N - 1);
             }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < kRing; i += kStep) fetch(i);
+    Eight sum{};
+#pragma unroll 1
+    for (int i = 0; i < count; i += kStep) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing / kStep - 1) : "memory");
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                if (i + j >= count) break;
-                if (keys[j] != key) {
-                    finish(false);
-                    key = keys[j];
-                    sum = Eight{};
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sum.x[k] = __fadd2_rn(sum.x[k], cols.pair(v[j], k));
+        for (int j = 0; j < kStep; ++j) {
+            if (i + j >= count) break;
+            const T* row = dout;                           // its alignment is all that counts
+            if constexpr (!VEC && sizeof(T) == 2) row += static_cast<int64_t>(token_at(i + j)) * a.stride;
+            if (on) cols.add(sum, mine + (i % kRing + j) * (kVecs * kRowThreads), row);
+            if (!(ends >> (i + j) & 1)) continue;
+            const uint32_t key = key_at(i + j);
+            if (on) {
+                if (key == first_key && from_before) cols.write(a.r.parts + (piece * 2) * a.r.columns, sum);
+                else if (i + j == count - 1 && goes_on) cols.write(a.r.parts + (piece * 2 + 1) * a.r.columns, sum);
+                else cols.write_scaled(a.dtable + static_cast<int64_t>(key) * a.e.dim, sum, a.e.scale, a.accumulate);
             }
+            sum = Eight{};
         }
-        finish(true);
+        fetch(i + kRing);
     }
-    if (goes_on && !(first_key == last_key && from_before) && blockIdx.y == 0 && threadIdx.x % a.group == 0)
-        a.r.list[atomicAdd(a.r.count, 1)] = static_cast<int32_t>(piece);
-}
-
-// A CTA for 128 columns of one id: warps take its parts in turn.
-constexpr int kJoinColumns = 128;
-
-__global__ void __launch_bounds__(kRowThreads) join_kernel(const __grid_constant__ SumArgs a)
-{
-    constexpr int kWarps = kRowThreads / 32;
-    __shared__ float4 sums[kWarps][kJoinColumns / 4];
-    wait_for_previous();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t N = a.e.tokens, pieces = (N + kPiece - 1) / kPiece;
-    const int64_t tiles = (a.e.dim + kJoinColumns - 1) / kJoinColumns, total = *a.r.count * tiles;
-    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-        const int64_t piece = a.r.list[i / tiles];
-        const int64_t c0 = (i % tiles) * kJoinColumns;
-        const uint32_t key = key_of(a.r.sorted[(piece + 1) * kPiece]);
-        // the first piece behind it that does not begin with the id: 32 places at a time
-        int64_t lo = piece + 2, hi = pieces;
+    if (goes_on && !(first_key == last_key && from_before) && blockIdx.x % a.tiles == 0 && tid < 32) {
+        // a long id begins here: the first piece behind it that does not begin with it, 32 places at a time
+        int64_t lo = piece + 2, hi = a.r.pieces;
         while (lo < hi) {
             const int64_t step = (hi - lo + 31) / 32, at = lo + lane * step;
-            const uint32_t less = __ballot_sync(~0u, at < hi && key_of(a.r.sorted[at * kPiece]) == key);
-            const int n = __popc(less);                    // ones, then zeros
+            const int n = __popc(__ballot_sync(~0u, at < hi && key_of(entry_at(a.r.sorted, at * P, N, none)) == last_key));
             if (n == 0) break;
             hi = min(hi, lo + n * step);
             lo += (n - 1) * step + 1;
         }
-        const int64_t parts = lo - piece;                  // its own, and one of each piece behind it
-        const int64_t c = c0 + lane * 4;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (c < a.r.columns) {
-#pragma unroll 4
-            for (int64_t q = warp; q < parts; q += kWarps) {
-                const float4 x = *reinterpret_cast<const float4*>(a.r.parts + ((piece + q) * 2 + (q == 0)) * a.r.columns + c);
-                sum = make_float4(__fadd_rn(sum.x, x.x), __fadd_rn(sum.y, x.y), __fadd_rn(sum.z, x.z), __fadd_rn(sum.w, x.w));
-            }
+        const int parts = static_cast<int>(lo - piece);
+        const int many = parts > kFewParts;
+        if (lane == 0) a.r.list[many * a.r.pieces + atomicAdd(a.r.count + many, 1)] = make_int2(static_cast<int>(piece), parts);
+    }
+}
+
+// The parts of one id, a CTA for some of its columns: 128 of an id of few parts,
+// 16 of one of many; the CTA's rows of threads take the parts in turn.
+template <int COLUMNS>
+__device__ __forceinline__ void join_parts(const SumArgs& a, int2 what, int64_t c0, float* shared)
+{
+    constexpr int kAcross = COLUMNS / 4, kRows = kRowThreads / kAcross;
+    const int x = threadIdx.x % kAcross, y = threadIdx.x / kAcross;
+    const int64_t piece = what.x, c = c0 + x * 4;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < a.r.columns) {
+#pragma unroll 8
+        for (int q = y; q < what.y; q += kRows) {          // its own part, and one of each piece behind it
+            const float4 p = *reinterpret_cast<const float4*>(a.r.parts + ((piece + q) * 2 + (q == 0)) * a.r.columns + c);
+            sum = make_float4(__fadd_rn(sum.x, p.x), __fadd_rn(sum.y, p.y), __fadd_rn(sum.z, p.z), __fadd_rn(sum.w, p.w));
         }
-        sums[warp][lane] = sum;
-        __syncthreads();
-        if (threadIdx.x < kJoinColumns && c0 + threadIdx.x < a.e.dim) {
-            float x = 0.0f;
-            for (int w = 0; w < kWarps; ++w) x = __fadd_rn(x, reinterpret_cast<const float*>(sums[w])[threadIdx.x]);
-            uint16_t* to = a.dtable + static_cast<int64_t>(key) * a.e.dim + c0 + threadIdx.x;
-            store1(to, a.accumulate ? __fmaf_rn(a.e.scale, x, load1(to)) : __fmul_rn(a.e.scale, x));
-        }
-        __syncthreads();
+    }
+    reinterpret_cast<float4*>(shared)[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < COLUMNS && c0 + threadIdx.x < a.e.dim) {
+        float s = 0.0f;
+        for (int r = 0; r < min(kRows, what.y); ++r) s = __fadd_rn(s, shared[r * COLUMNS + threadIdx.x]);
+        const uint32_t key = key_of(a.r.sorted[(piece + 1) * a.r.piece]);
+        uint16_t* to = a.dtable + static_cast<int64_t>(key) * a.e.dim + c0 + threadIdx.x;
+        store1(to, a.accumulate ? __fmaf_rn(a.e.scale, s, load1(to)) : __fmul_rn(a.e.scale, s));
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kRowThreads) join_kernel(const __grid_constant__ SumArgs a)
+{
+    __shared__ __align__(16) float shared[kRowThreads * 4];
+    wait_for_previous();
+    const int64_t few = (a.e.dim + 127) / 128, many = (a.e.dim + 15) / 16;
+    const int64_t first = a.r.count[1] * many, total = first + a.r.count[0] * few;
+    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+        if (i < first) join_parts<16>(a, a.r.list[a.r.pieces + i / many], i % many * 16, shared);
+        else join_parts<128>(a, a.r.list[(i - first) / few], (i - first) % few * 128, shared);
     }
 }
 
@@ -602,7 +755,7 @@ cudaError_t clusters_at_once(int* out)
 }
 
 // The kernel after another one of the same call (wait_for_previous).
-cudaError_t launch_after(void (*kernel)(SumArgs), dim3 grid, cudaStream_t st, const SumArgs& a)
+cudaError_t launch_after(void (*kernel)(SumArgs), dim3 grid, int shared, cudaStream_t st, const SumArgs& a)
 {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -610,10 +763,30 @@ cudaError_t launch_after(void (*kernel)(SumArgs), dim3 grid, cudaStream_t st, co
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// What the sort takes, and what is written meanwhile.
+constexpr double kSortUs = 8.0, kSortTokenUs = 2.0e-4, kFillBytesUs = 5.5e6;
+constexpr int64_t kFillBytes = 1 << 17;        // of a CTA of sum_kernel
+
+using SumKernel = void (*)(SumArgs);
+struct SumShape {
+    SumKernel kernel;
+    int shared;
+};
+
+template <typename T, bool VEC>
+SumShape sum_shape() { return {sum_kernel<T, VEC>, kSumShared<T, VEC>}; }
+
+SumShape sum_shape(bool f32, bool vec)
+{
+    return f32 ? (vec ? sum_shape<float, true>() : sum_shape<float, false>())
+               : (vec ? sum_shape<uint16_t, true>() : sum_shape<uint16_t, false>());
 }
 
 }  // namespace
@@ -622,6 +795,11 @@ cudaError_t prepare_embed()
 {
     int n = 0;
     cudaError_t e = clusters_at_once(&n);
+    for (bool f32 : {false, true})
+        for (bool vec : {false, true}) {
+            const SumShape s = sum_shape(f32, vec);
+            if (e == cudaSuccess) e = persistent_grid(reinterpret_cast<const void*>(s.kernel), kRowThreads, s.shared, &n);
+        }
     return e == cudaSuccess ? persistent_grid(reinterpret_cast<const void*>(join_kernel), kRowThreads, 0, &n) : e;
 }
 
@@ -635,8 +813,12 @@ int64_t embed_workspace(const q8_embedding& e) { return e.tokens == 0 ? 0 : room
 cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64_t dout_stride, uint16_t* dtable,
                                   bool accumulate, void* workspace, cudaStream_t st)
 {
+    const int size = e.dtype == Q8_F32 ? 4 : 2;
+    const bool vec = e.dim % 8 == 0 && on16(dtable) && on16(dout) && (e.tokens == 1 || dout_stride * size % 16 == 0);
+    const SumShape sum = sum_shape(size == 4, vec);
     int clusters = 0, joins = 0;
     cudaError_t err = clusters_at_once(&clusters);
+    if (err == cudaSuccess) err = persistent_grid(reinterpret_cast<const void*>(sum.kernel), kRowThreads, sum.shared, &joins);
     if (err == cudaSuccess) err = persistent_grid(reinterpret_cast<const void*>(join_kernel), kRowThreads, 0, &joins);
     if (err != cudaSuccess) return err;
     const Room room = room_of(e, workspace);
@@ -649,7 +831,10 @@ cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64
     while (e.vocab >> bits) ++bits;            // vocab itself is the key of ids outside the table
     o.passes = (bits + kDigitBits - 1) / kDigitBits;
     o.digit = (bits + o.passes - 1) / o.passes;
-    o.fill = accumulate ? 0 : 2;
+    // as many rows as are written while the tokens are sorted
+    const double sort_us = kSortUs + kSortTokenUs * static_cast<double>(e.tokens);
+    const int64_t rows = static_cast<int64_t>(sort_us * kFillBytesUs / (2.0 * static_cast<double>(e.dim)));
+    o.fill = accumulate ? 0 : std::min(e.vocab, rows);
     const int ctas = accumulate ? kCluster : std::max(2, clusters) * kCluster;
     cudaLaunchAttribute attr{};
     const cudaLaunchConfig_t cfg = order_config(&attr, ctas, st);
@@ -662,17 +847,16 @@ cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64
     s.stride = dout_stride;
     s.dtable = dtable;
     s.accumulate = accumulate;
-    s.group = 32;
-    while (s.group < kRowThreads && s.group * 8 < e.dim) s.group *= 2;
-    const int size = e.dtype == Q8_F32 ? 4 : 2;
-    const bool vec = e.dim % 8 == 0 && on16(dtable) && on16(dout) && (e.tokens == 1 || dout_stride * size % 16 == 0);
-    const int64_t pieces = (e.tokens + kPiece - 1) / kPiece, each = kRowThreads / s.group;
-    const dim3 grid(static_cast<unsigned>((pieces + each - 1) / each),
-                    static_cast<unsigned>(std::min<int64_t>((e.dim + s.group * 8 - 1) / (s.group * 8), 65535)));
-    const auto sum = size == 4 ? (vec ? sum_kernel<float, true> : sum_kernel<float, false>)
-                               : (vec ? sum_kernel<uint16_t, true> : sum_kernel<uint16_t, false>);
-    if ((err = launch_after(sum, grid, st, s)) != cudaSuccess) return err;
-    return launch_after(join_kernel, dim3(static_cast<unsigned>(joins)), st, s);
+    s.group = group_of(e);
+    s.tiles = static_cast<int>((e.dim + s.group * 8 - 1) / (s.group * 8));
+    const int64_t each = kRowThreads / s.group;
+    s.sums = (room.pieces + each - 1) / each * s.tiles;
+    s.filled = o.fill;
+    s.fill_rows = std::max<int64_t>(1, kFillBytes / 2 / e.dim);
+    const int64_t grid = s.sums + (accumulate ? 0 : (e.vocab - o.fill + s.fill_rows - 1) / s.fill_rows);
+    if (grid > std::numeric_limits<int32_t>::max()) return cudaErrorInvalidConfiguration;
+    if ((err = launch_after(sum.kernel, dim3(static_cast<unsigned>(grid)), sum.shared, st, s)) != cudaSuccess) return err;
+    return launch_after(join_kernel, dim3(static_cast<unsigned>(joins / 2)), 0, st, s);
 }
 
 }  // namespace q8
