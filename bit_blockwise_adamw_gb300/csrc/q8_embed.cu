@@ -49,10 +49,12 @@ __device__ __forceinline__ uint32_t bf16_pair(float2 x)
     return static_cast<uint32_t>(float_to_bf16(x.x)) | static_cast<uint32_t>(float_to_bf16(x.y)) << 16;
 }
 
-__device__ __forceinline__ void write8(uint16_t* p, const Eight& v)
+__device__ __forceinline__ uint4 vector_of(const Eight& v)
 {
-    *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v.x[0]), bf16_pair(v.x[1]), bf16_pair(v.x[2]), bf16_pair(v.x[3]));
+    return make_uint4(bf16_pair(v.x[0]), bf16_pair(v.x[1]), bf16_pair(v.x[2]), bf16_pair(v.x[3]));
 }
+
+__device__ __forceinline__ void write8(uint16_t* p, const Eight& v) { *reinterpret_cast<uint4*>(p) = vector_of(v); }
 
 __device__ __forceinline__ void write8(float* p, const Eight& v)
 {
@@ -60,13 +62,25 @@ __device__ __forceinline__ void write8(float* p, const Eight& v)
     reinterpret_cast<float4*>(p)[1] = make_float4(v.x[2].x, v.x[2].y, v.x[3].x, v.x[3].y);
 }
 
+// The same, of which L2 need not keep anything.
+__device__ __forceinline__ void stream8(uint16_t* p, const Eight& v) { __stcs(reinterpret_cast<uint4*>(p), vector_of(v)); }
+
+__device__ __forceinline__ void stream8(float* p, const Eight& v)
+{
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v.x[0].x, v.x[0].y, v.x[1].x, v.x[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v.x[2].x, v.x[2].y, v.x[3].x, v.x[3].y));
+}
+
 // ----------------------------------------------------------------------- lookup
 
+constexpr int64_t kStreamBytes = 64 << 20;     // half of L2
 constexpr int kTile = 4;                       // vectors of a thread, all in flight
 
 // Rows of whole 16-byte vectors: the output as one run of vectors, kTile *
-// kRowThreads of them to a CTA at a time.
-template <typename T>
+// kRowThreads of them to a CTA at a time.  STREAM: an output that L2 would not
+// hold for its reader leaves L2 to the table's rows (16384 x 4096: 31.9 us,
+// else 34.3).
+template <typename T, bool STREAM>
 __global__ void __launch_bounds__(kRowThreads) lookup_kernel(q8_embedding e, const uint16_t* table, T* out, int64_t out_stride)
 {
     const uint32_t width = static_cast<uint32_t>(e.dim / 8);
@@ -95,7 +109,8 @@ __global__ void __launch_bounds__(kRowThreads) lookup_kernel(q8_embedding e, con
             Eight v{{bf16x2(w[j].x), bf16x2(w[j].y), bf16x2(w[j].z), bf16x2(w[j].w)}};
 #pragma unroll
             for (int k = 0; k < 4; ++k) v.x[k] = __fmul2_rn(v.x[k], splat(e.scale));
-            write8(to[j], v);
+            if (STREAM) stream8(to[j], v);
+            else write8(to[j], v);
         }
     }
 }
@@ -124,6 +139,8 @@ __global__ void __launch_bounds__(kRowThreads) lookup_odd_kernel(q8_embedding e,
 // ---------------------------------------------------------------------- gradient
 
 constexpr int kFewParts = 32;
+constexpr int64_t kClusterTokens = 32768;      // sorted by one cluster, at most
+constexpr int kMaxSorters = 128;               // CTAs that sort more of them (152 or 96: 2 us more at 262144)
 constexpr int kCluster = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -138,6 +155,8 @@ struct Room {
     uint64_t* sorted;          // [tokens]: id << 32 | token, ids outside the table as vocab
     uint64_t* other;           // the sort's second buffer
     int32_t* count;            // [2]: ids whose parts are to be joined, of few parts and of many
+    uint8_t* present;          // [vocab]: 1 where a token has the row
+    uint32_t* digits;          // [SMs][kBins]: the sort's counts, of more than kClusterTokens
     int2* list;                // [2][pieces]: the piece that each of them begins in, and its parts
     float* parts;              // [pieces][2][columns]: of an id from before the piece; of one that goes on behind it
     int64_t columns;           // dim, to whole vectors
@@ -180,6 +199,8 @@ Room room_of(const q8_embedding& e, void* workspace)
     r.sorted = reinterpret_cast<uint64_t*>(take(e.tokens * 8));
     r.other = reinterpret_cast<uint64_t*>(take(e.tokens * 8));
     r.count = reinterpret_cast<int32_t*>(take(8));
+    r.present = reinterpret_cast<uint8_t*>(take(e.vocab));
+    if (e.tokens > kClusterTokens) r.digits = reinterpret_cast<uint32_t*>(take(kMaxSorters * kBins * 4));
     r.list = reinterpret_cast<int2*>(take(2 * pieces * 8));
     r.parts = reinterpret_cast<float*>(take(pieces * 2 * r.columns * 4));
     r.bytes = at;
@@ -191,6 +212,8 @@ struct OrderArgs {
     Room r;
     uint16_t* dtable;
     int32_t passes, digit;     // of the sort: passes, bits of each
+    int32_t pass;              // count_kernel, place_kernel: the one at hand
+    int32_t clear, note;       // r.present is cleared; the sort notes there what it meets
     int64_t fill;              // the table's rows [0, fill) get their zeros here
 };
 
@@ -200,6 +223,8 @@ __device__ __forceinline__ uint32_t cluster_read(const uint32_t* p, uint32_t ran
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_addr(smem_addr(p), rank)) : "memory");
     return v;
 }
+
+__device__ __forceinline__ uint32_t key_of(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
 // The warp's lanes that have this lane's digit (of `bits` bits), among those that
 // are on: a ballot for each bit.  __match_any_sync took four times as long.
@@ -215,81 +240,174 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t d, bool on, int bits)
     return same;
 }
 
-// One CTA's part of the sort: the tokens [lo, hi) of each pass's order.
-__device__ void sort_tokens(const OrderArgs& a, uint32_t (*counts)[kBins])
-{
-    __shared__ uint32_t hist[kBins], sums[kSortWarps];
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const uint32_t rank = cluster_rank();
-    const int64_t T = a.e.tokens;
-    const int64_t lo = T * rank / kCluster, hi = T * (rank + 1) / kCluster;
-    const int items = static_cast<int>(max(int64_t(1), min(int64_t(kItems), (hi - lo + kSortThreads - 1) / kSortThreads)));
-    const int bins = 1 << a.digit;
-    if (rank == 0 && tid < 2) a.r.count[tid] = 0;
-    const int64_t tile = static_cast<int64_t>(kSortThreads) * items;
-    const bool single = hi - lo <= tile;       // its tokens then stay in registers from counting to placing
+// One pass of the sort, as one CTA sees it: it owns the tokens [lo, hi) of the
+// order that the pass before left (before the first, that of the ids), takes
+// them in tiles, a warp `items` times 32 consecutive ones, and puts each behind
+// those of its digit that came before.
+struct Pass {
+    uint8_t* present;          // of the first pass: the rows that it meets are noted here
+    const int64_t* ids;        // of the first pass
+    const uint64_t* from;      // of the others
+    uint64_t* to;
+    int64_t vocab, lo, hi;
+    int shift, bits, items;
     uint64_t x[kItems];
     uint32_t place[kItems];
-    for (int pass = 0; pass < a.passes; ++pass) {
-        const uint64_t* from = (a.passes - pass) % 2 ? a.r.other : a.r.sorted;
-        uint64_t* to = (a.passes - pass) % 2 ? a.r.sorted : a.r.other;
-        const int shift = 32 + pass * a.digit;
-        const auto load = [&](int64_t at) {
+
+    __device__ __forceinline__ int64_t tile() const { return static_cast<int64_t>(kSortThreads) * items; }
+
+    __device__ __forceinline__ void load(int64_t at)
+    {
 #pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-                const int64_t i = at + (warp * items + j) * 32 + lane;
-                if (j >= items || i >= hi) continue;
-                if (pass > 0) {
-                    x[j] = __ldcg(reinterpret_cast<const unsigned long long*>(from) + i);
-                } else {
-                    const int64_t id = a.e.ids[i];
-                    const uint32_t key = static_cast<uint32_t>(id >= 0 && id < a.e.vocab ? id : a.e.vocab);
-                    x[j] = static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(i);
-                }
+        for (int j = 0; j < kItems; ++j) {
+            const int64_t i = at + (threadIdx.x / 32 * items + j) * 32 + threadIdx.x % 32;
+            if (j >= items || i >= hi) continue;
+            if (!ids) {
+                x[j] = __ldcg(reinterpret_cast<const unsigned long long*>(from) + i);
+            } else {
+                const int64_t id = ids[i];
+                const uint32_t key = static_cast<uint32_t>(id >= 0 && id < vocab ? id : vocab);
+                x[j] = static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(i);
             }
-        };
-        const auto digit = [&](int64_t at, int j) {
-            return at + (warp * items + j) * 32 + lane < hi ? static_cast<uint32_t>(x[j] >> shift) & (bins - 1) : ~0u;
-        };
-        // each token's place among its warp's of the same digit, and the warp's counts
-        const auto rank_tile = [&](int64_t at) {
-            __syncwarp();                      // its lanes have read their places of the tile before
-            for (int d = lane; d < bins; d += 32) counts[warp][d] = 0;
+        }
+    }
+    __device__ __forceinline__ uint32_t digit(int64_t at, int j) const
+    {
+        const int64_t i = at + (threadIdx.x / 32 * items + j) * 32 + threadIdx.x % 32;
+        return i < hi ? static_cast<uint32_t>(x[j] >> shift) & ((1u << bits) - 1) : ~0u;
+    }
+    // Each token's place among its warp's of the same digit, and the warp's counts.
+    __device__ __forceinline__ void rank(int64_t at, uint32_t (*counts)[kBins])
+    {
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+        __syncwarp();                          // its lanes have read their places of the tile before
+        for (int d = lane; d < 1 << bits; d += 32) counts[warp][d] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            if (j >= items) break;
+            const uint32_t d = digit(at, j), same = same_digit(d, d != ~0u, bits);
+            const uint32_t seen = d != ~0u ? counts[warp][d] : 0;
+            place[j] = seen + __popc(same & ((1u << lane) - 1));
             __syncwarp();
+            if (d != ~0u && lane == __ffs(same) - 1) counts[warp][d] = seen + __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+    }
+    // The CTA's counts, to thread d < 2^bits those of digit d; its tokens, if
+    // they are one tile, ranked.
+    __device__ __forceinline__ uint32_t count(uint32_t (*counts)[kBins], uint32_t* hist)
+    {
+        const int tid = threadIdx.x, bins = 1 << bits;
+        if (hi - lo <= tile()) {
+            load(lo);
+            rank(lo, counts);
+            uint32_t n = 0;
+            if (tid < bins) {
+#pragma unroll 8
+                for (int w = 0; w < kSortWarps; ++w) n += counts[w][tid];
+            }
+            return n;
+        }
+        for (int d = tid; d < bins; d += kSortThreads) hist[d] = 0;
+        __syncthreads();
+        for (int64_t at = lo; at < hi; at += tile()) {
+            load(at);
 #pragma unroll
             for (int j = 0; j < kItems; ++j) {
                 if (j >= items) break;
-                const uint32_t d = digit(at, j), same = same_digit(d, d != ~0u, a.digit);
-                const uint32_t seen = d != ~0u ? counts[warp][d] : 0;
-                place[j] = seen + __popc(same & ((1u << lane) - 1));
-                __syncwarp();
-                if (d != ~0u && lane == __ffs(same) - 1) counts[warp][d] = seen + __popc(same);
-                __syncwarp();
-            }
-            __syncthreads();
-        };
-        if (single) {
-            load(lo);
-            rank_tile(lo);
-            if (tid < bins) {
-                uint32_t n = 0;
-#pragma unroll 8
-                for (int w = 0; w < kSortWarps; ++w) n += counts[w][tid];
-                hist[tid] = n;
-            }
-        } else {
-            for (int d = tid; d < bins; d += kSortThreads) hist[d] = 0;
-            __syncthreads();
-            for (int64_t at = lo; at < hi; at += tile) {
-                load(at);
-#pragma unroll
-                for (int j = 0; j < kItems; ++j) {
-                    if (j >= items) break;
-                    const uint32_t d = digit(at, j), same = same_digit(d, d != ~0u, a.digit);
-                    if (d != ~0u && lane == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
-                }
+                const uint32_t d = digit(at, j), same = same_digit(d, d != ~0u, bits);
+                if (d != ~0u && tid % 32 == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
             }
         }
+        __syncthreads();
+        return tid < bins ? hist[tid] : 0;
+    }
+    // Puts the tokens in their places; base: to thread d the first one of digit d
+    // in this CTA.  ranked: they are one tile, and count() has just ranked it.
+    __device__ __forceinline__ void scatter(uint32_t (*counts)[kBins], uint32_t base, bool ranked)
+    {
+        for (int64_t at = lo; at < hi; at += tile()) {
+            if (!ranked) {
+                load(at);
+                rank(at, counts);
+            }
+            if (threadIdx.x < 1 << bits) {
+#pragma unroll 8
+                for (int w = 0; w < kSortWarps; ++w) {
+                    const uint32_t n = counts[w][threadIdx.x];
+                    counts[w][threadIdx.x] = base;
+                    base += n;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                if (j >= items) break;
+                const uint32_t d = digit(at, j);
+                if (d == ~0u) continue;
+                to[counts[threadIdx.x / 32][d] + place[j]] = x[j];
+                if (present && key_of(x[j]) < vocab) present[key_of(x[j])] = 1;
+            }
+        }
+    }
+};
+
+// Pass `pass`, of which CTA `cta` of `ctas` has its share.
+__device__ __forceinline__ Pass pass_of(const OrderArgs& a, int pass, int64_t cta, int64_t ctas)
+{
+    Pass p;
+    p.ids = pass == 0 ? a.e.ids : nullptr;
+    p.present = pass == 0 && a.note ? a.r.present : nullptr;
+    p.from = (a.passes - pass) % 2 ? a.r.other : a.r.sorted;
+    p.to = (a.passes - pass) % 2 ? a.r.sorted : a.r.other;
+    p.vocab = a.e.vocab;
+    p.lo = a.e.tokens * cta / ctas;
+    p.hi = a.e.tokens * (cta + 1) / ctas;
+    p.shift = 32 + pass * a.digit;
+    p.bits = a.digit;
+    p.items = static_cast<int>(max(int64_t(1), min(int64_t(kItems), (p.hi - p.lo + kSortThreads - 1) / kSortThreads)));
+    return p;
+}
+
+// The sum of `x` over the threads before this one.
+__device__ __forceinline__ uint32_t sum_before(uint32_t x, uint32_t* sums)
+{
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t sum = x;
+    for (int o = 1; o < 32; o *= 2) {
+        const uint32_t s = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += s;
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x < kBins)
+        for (int w = 0; w < warp; ++w) sum += sums[w];
+    __syncthreads();
+    return sum - x;
+}
+
+__device__ __forceinline__ void clear_present(const OrderArgs& a, int64_t cta, int64_t ctas)
+{
+    if (!a.clear) return;
+    uint4* p = reinterpret_cast<uint4*>(a.r.present);        // up to its last, whole vector
+    const int64_t n = (a.e.vocab + 15) / 16;
+    for (int64_t i = cta * kSortThreads + threadIdx.x; i < n; i += ctas * kSortThreads) p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// The sort by one cluster.
+__device__ void sort_tokens(const OrderArgs& a, uint32_t (*counts)[kBins])
+{
+    __shared__ uint32_t hist[kBins], sums[kSortWarps];
+    const int tid = threadIdx.x, bins = 1 << a.digit;
+    const uint32_t rank = cluster_rank();
+    if (rank == 0 && tid < 2) a.r.count[tid] = 0;
+    clear_present(a, rank, kCluster);          // set after a barrier of the cluster
+    for (int pass = 0; pass < a.passes; ++pass) {
+        Pass p = pass_of(a, pass, rank, kCluster);
+        const uint32_t n = p.count(counts, hist);
+        if (tid < bins) hist[tid] = n;
         cluster_sync();
         // a digit's first place: all smaller digits, and its own in the CTAs before
         uint32_t all = 0, before = 0;
@@ -301,37 +419,7 @@ __device__ void sort_tokens(const OrderArgs& a, uint32_t (*counts)[kBins])
                 before += c < rank ? h : 0;
             }
         }
-        uint32_t sum = all;
-        for (int o = 1; o < 32; o *= 2) {
-            const uint32_t s = __shfl_up_sync(~0u, sum, o);
-            if (lane >= o) sum += s;
-        }
-        if (lane == 31) sums[warp] = sum;
-        __syncthreads();
-        if (tid < bins)
-            for (int w = 0; w < warp; ++w) sum += sums[w];
-        uint32_t base = sum - all + before;    // of digit tid
-        for (int64_t at = lo; at < hi; at += tile) {
-            if (!single) {
-                load(at);
-                rank_tile(at);
-            }
-            if (tid < bins) {
-#pragma unroll 8
-                for (int w = 0; w < kSortWarps; ++w) {
-                    const uint32_t n = counts[w][tid];
-                    counts[w][tid] = base;
-                    base += n;
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-                if (j >= items) break;
-                const uint32_t d = digit(at, j);
-                if (d != ~0u) to[counts[warp][d] + place[j]] = x[j];
-            }
-        }
+        p.scatter(counts, sum_before(all, sums) + before, p.hi - p.lo <= p.tile());
         cluster_sync();                        // what all CTAs wrote is there, and their counts are read
     }
 }
@@ -346,6 +434,22 @@ __device__ __forceinline__ void zero_run(uint16_t* p, int64_t n, int lane)
 #pragma unroll 4
     for (int64_t i = lane; i < vecs; i += 32) q[i] = make_uint4(0, 0, 0, 0);
     if (lead + vecs * 8 + lane < n) p[lead + vecs * 8 + lane] = 0;
+}
+
+// Zeros into those of the table's rows first + [begin, end) that have no bit in
+// the map: run by run, one warp.
+__device__ __forceinline__ void zero_absent(uint16_t* table, int64_t dim, int64_t first, int begin, int end, const uint32_t* map, int lane)
+{
+    for (int r = begin; r < end;) {
+        if (map[r / 32] >> (r % 32) & 1) {
+            ++r;
+            continue;
+        }
+        int stop = r + 1;
+        while (stop < end && !(map[stop / 32] >> (stop % 32) & 1)) ++stop;
+        zero_run(table + (first + r) * dim, (stop - r) * dim, lane);
+        r = stop;
+    }
 }
 
 // One CTA's part of the zeros: the table's rows [begin, end) that no token has.
@@ -364,9 +468,8 @@ __device__ void fill_rows(const OrderArgs& a, uint32_t* map, int64_t cta, int64_
             if (r < static_cast<uint64_t>(rows) && !(static_cast<volatile uint32_t*>(map)[r / 32] >> (r % 32) & 1)) atomicOr(&map[r / 32], 1u << (r % 32));
         }
         __syncthreads();
-        for (int64_t r = warp; r < rows; r += kSortWarps) {
-            if (!(map[r / 32] >> (r % 32) & 1)) zero_run(a.dtable + (first + r) * a.e.dim, a.e.dim, lane);
-        }
+        zero_absent(a.dtable, a.e.dim, first, static_cast<int>(rows * warp / kSortWarps), static_cast<int>(rows * (warp + 1) / kSortWarps),
+                    map, lane);
         __syncthreads();
     }
 }
@@ -382,6 +485,55 @@ __global__ void __launch_bounds__(kSortThreads) order_kernel(const __grid_consta
     else fill_rows(a, shared, blockIdx.x - kCluster, gridDim.x - kCluster);
 }
 
+// The same sort of more tokens, by all SMs: two launches a pass, the first of
+// which leaves the CTAs' counts in the workspace.
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ OrderArgs a)
+{
+    extern __shared__ __align__(16) uint32_t shared[];
+    __shared__ uint32_t hist[kBins];
+    let_next_start();
+    wait_for_previous();
+    if (blockIdx.x == 0 && threadIdx.x < 2) a.r.count[threadIdx.x] = 0;
+    if (a.pass == 0) clear_present(a, blockIdx.x, gridDim.x);
+    Pass p = pass_of(a, a.pass, blockIdx.x, gridDim.x);
+    const uint32_t n = p.count(reinterpret_cast<uint32_t(*)[kBins]>(shared), hist);
+    if (threadIdx.x < 1 << a.digit) a.r.digits[blockIdx.x * kBins + threadIdx.x] = n;
+}
+
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_constant__ OrderArgs a)
+{
+    extern __shared__ __align__(16) uint32_t shared[];
+    __shared__ uint32_t sums[kSortWarps];
+    uint32_t(*counts)[kBins] = reinterpret_cast<uint32_t(*)[kBins]>(shared);
+    let_next_start();
+    wait_for_previous();
+    Pass p = pass_of(a, a.pass, blockIdx.x, gridDim.x);
+    const bool single = p.hi - p.lo <= p.tile();
+    if (single) p.load(p.lo);
+    // each digit's counts of all CTAs, and of those before: a share of the CTAs
+    // for each of kSortThreads / bins threads
+    const int bins = 1 << a.digit, shares = kSortThreads / bins, d = threadIdx.x % bins, share = threadIdx.x / bins;
+    uint32_t all = 0, before = 0;
+#pragma unroll 32
+    for (int c = share; c < static_cast<int>(gridDim.x); c += shares) {
+        const uint32_t n = __ldcg(a.r.digits + c * kBins + d);
+        all += n;
+        before += c < static_cast<int>(blockIdx.x) ? n : 0;
+    }
+    shared[threadIdx.x] = all;
+    shared[kSortThreads + threadIdx.x] = before;
+    __syncthreads();
+    all = before = 0;
+    if (threadIdx.x < bins)
+        for (int i = 0; i < shares; ++i) {
+            all += shared[i * bins + d];
+            before += shared[kSortThreads + i * bins + d];
+        }
+    const uint32_t base = sum_before(all, sums) + before;
+    if (single) p.rank(p.lo, counts);
+    p.scatter(counts, base, single);
+}
+
 struct SumArgs {
     q8_embedding e;
     Room r;
@@ -389,12 +541,11 @@ struct SumArgs {
     int64_t stride;
     uint16_t* dtable;
     int64_t filled, fill_rows; // the table's rows from `filled` on get their zeros here, so many to a CTA
-    int64_t sums;              // CTAs that add up; the others write zeros
+    int64_t sums, joins;       // CTAs that add up, and that join; those behind them write zeros
+    int32_t late;              // the zeros are written beside the joins: sum_kernel notes the rows that it meets
     int32_t accumulate;
     int32_t group, tiles;      // threads that share a piece's columns, and tiles of 8 * group columns
 };
-
-__device__ __forceinline__ uint32_t key_of(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
 // A thread's eight columns: VEC, contiguous; else every step-th, of bf16 in
 // pairs.  Rows on their way wait in the thread's own slots of shared memory (no
@@ -537,19 +688,13 @@ __device__ void fill_absent(const SumArgs& a, int64_t begin, int64_t end)
     __shared__ uint32_t present[kRowThreads / 32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     for (int64_t first = begin; first < end; first += kRowThreads) {
-        const int64_t row = first + threadIdx.x;
-        int64_t lo = 0, hi = row < end ? a.e.tokens : 0;   // the first token whose id is not below the row
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if (key_of(a.r.sorted[mid]) < row) lo = mid + 1; else hi = mid;
-        }
-        const uint32_t some = __ballot_sync(~0u, row < end && lo < a.e.tokens && key_of(a.r.sorted[lo]) == row);
+        const uint32_t some = __ballot_sync(~0u, first + threadIdx.x < end && a.r.present[first + threadIdx.x]);
         __syncthreads();
         if (lane == 0) present[warp] = some;
         __syncthreads();
         const int rows = static_cast<int>(min(int64_t(kRowThreads), end - first));
-        for (int r = warp; r < rows; r += kRowThreads / 32)
-            if (!(present[r / 32] >> (r % 32) & 1)) zero_run(a.dtable + (first + r) * a.e.dim, a.e.dim, lane);
+        constexpr int kWarps = kRowThreads / 32;
+        zero_absent(a.dtable, a.e.dim, first, rows * warp / kWarps, rows * (warp + 1) / kWarps, present, lane);
     }
 }
 
@@ -634,8 +779,13 @@ __global__ void __launch_bounds__(kRowThreads, 3) sum_kernel(const __grid_consta
             if (!(ends >> (i + j) & 1)) continue;
             const uint32_t key = key_at(i + j);
             if (on) {
-                if (key == first_key && from_before) cols.write(a.r.parts + (piece * 2) * a.r.columns, sum);
-                else if (i + j == count - 1 && goes_on) cols.write(a.r.parts + (piece * 2 + 1) * a.r.columns, sum);
+                if (key == first_key && from_before) {
+                    cols.write(a.r.parts + (piece * 2) * a.r.columns, sum);
+                    sum = Eight{};
+                    continue;
+                }
+                if (a.late && blockIdx.x % a.tiles == 0 && tid == 0) a.r.present[key] = 1;
+                if (i + j == count - 1 && goes_on) cols.write(a.r.parts + (piece * 2 + 1) * a.r.columns, sum);
                 else cols.write_scaled(a.dtable + static_cast<int64_t>(key) * a.e.dim, sum, a.e.scale, a.accumulate);
             }
             sum = Eight{};
@@ -658,43 +808,77 @@ __global__ void __launch_bounds__(kRowThreads, 3) sum_kernel(const __grid_consta
     }
 }
 
-// The parts of one id, a CTA for some of its columns: 128 of an id of few parts,
-// 16 of one of many; the CTA's rows of threads take the parts in turn.
-template <int COLUMNS>
-__device__ __forceinline__ void join_parts(const SumArgs& a, int2 what, int64_t c0, float* shared)
+__device__ __forceinline__ float4 part_of(const SumArgs& a, int64_t piece, int q, int64_t c)
 {
-    constexpr int kAcross = COLUMNS / 4, kRows = kRowThreads / kAcross;
-    const int x = threadIdx.x % kAcross, y = threadIdx.x / kAcross;
-    const int64_t piece = what.x, c = c0 + x * 4;
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < a.r.columns) {
-#pragma unroll 8
-        for (int q = y; q < what.y; q += kRows) {          // its own part, and one of each piece behind it
-            const float4 p = *reinterpret_cast<const float4*>(a.r.parts + ((piece + q) * 2 + (q == 0)) * a.r.columns + c);
-            sum = make_float4(__fadd_rn(sum.x, p.x), __fadd_rn(sum.y, p.y), __fadd_rn(sum.z, p.z), __fadd_rn(sum.w, p.w));
-        }
-    }
-    reinterpret_cast<float4*>(shared)[threadIdx.x] = sum;
-    __syncthreads();
-    if (threadIdx.x < COLUMNS && c0 + threadIdx.x < a.e.dim) {
-        float s = 0.0f;
-        for (int r = 0; r < min(kRows, what.y); ++r) s = __fadd_rn(s, shared[r * COLUMNS + threadIdx.x]);
-        const uint32_t key = key_of(a.r.sorted[(piece + 1) * a.r.piece]);
-        uint16_t* to = a.dtable + static_cast<int64_t>(key) * a.e.dim + c0 + threadIdx.x;
-        store1(to, a.accumulate ? __fmaf_rn(a.e.scale, s, load1(to)) : __fmul_rn(a.e.scale, s));
-    }
-    __syncthreads();
+    // its own part, then one of each piece behind it
+    return *reinterpret_cast<const float4*>(a.r.parts + ((piece + q) * 2 + (q == 0)) * a.r.columns + c);
 }
 
+__device__ __forceinline__ float4 add4(float4 x, float4 y)
+{
+    return make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+}
+
+__device__ __forceinline__ void write_joined(const SumArgs& a, uint32_t key, int64_t c, float x)
+{
+    if (c >= a.e.dim) return;
+    uint16_t* to = a.dtable + static_cast<int64_t>(key) * a.e.dim + c;
+    store1(to, a.accumulate ? __fmaf_rn(a.e.scale, x, load1(to)) : __fmul_rn(a.e.scale, x));
+}
+
+// Ids of many parts: a CTA for eight columns (a sector of 32 bytes) of one of
+// them; its 128 pairs of threads take the parts in turn.  Ids of few: a warp for
+// 32 columns, its four groups of lanes take the parts in turn.
 __global__ void __launch_bounds__(kRowThreads) join_kernel(const __grid_constant__ SumArgs a)
 {
-    __shared__ __align__(16) float shared[kRowThreads * 4];
+    constexpr int kPairs = kRowThreads / 2, kSums = kRowThreads / 8;
+    __shared__ __align__(16) float sums[kPairs * 8];
+    __shared__ float last[kSums * 8];
     wait_for_previous();
-    const int64_t few = (a.e.dim + 127) / 128, many = (a.e.dim + 15) / 16;
-    const int64_t first = a.r.count[1] * many, total = first + a.r.count[0] * few;
-    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-        if (i < first) join_parts<16>(a, a.r.list[a.r.pieces + i / many], i % many * 16, shared);
-        else join_parts<128>(a, a.r.list[(i - first) / few], (i - first) % few * 128, shared);
+    if (blockIdx.x >= a.joins) {
+        const int64_t begin = a.filled + (blockIdx.x - a.joins) * a.fill_rows;
+        fill_absent(a, begin, min(a.e.vocab, begin + a.fill_rows));
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid % 32;
+    const int64_t ctas = a.joins;
+    const int64_t wide = (a.e.dim + 31) / 32, narrow = (a.e.dim + 7) / 8;
+    const int64_t many = a.r.count[1] * narrow, few = a.r.count[0] * wide;
+    for (int64_t i = blockIdx.x; i < many; i += ctas) {
+        const int2 what = a.r.list[a.r.pieces + i / narrow];
+        const uint32_t key = key_of(a.r.sorted[(static_cast<int64_t>(what.x) + 1) * a.r.piece]);
+        const int64_t c0 = i % narrow * 8;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int q = tid / 2; q < what.y; q += kPairs) sum = add4(sum, part_of(a, what.x, q, c0 + tid % 2 * 4));
+        reinterpret_cast<float4*>(sums)[tid] = sum;
+        __syncthreads();
+        float x = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kPairs / kSums; ++r) x = __fadd_rn(x, sums[(tid / 8 * (kPairs / kSums) + r) * 8 + tid % 8]);
+        last[tid] = x;
+        __syncthreads();
+        if (tid < 8) {
+            x = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kSums; ++r) x = __fadd_rn(x, last[r * 8 + tid]);
+            write_joined(a, key, c0 + tid, x);
+        }
+    }
+    // begun with the CTAs that had one id of many parts less
+    const int64_t cta = (blockIdx.x + ctas - many % ctas) % ctas;
+    for (int64_t i = cta * (kRowThreads / 32) + tid / 32; i < few; i += ctas * (kRowThreads / 32)) {
+        const int2 what = a.r.list[i / wide];
+        const uint32_t key = key_of(a.r.sorted[(static_cast<int64_t>(what.x) + 1) * a.r.piece]);
+        const int64_t c0 = i % wide * 32, c = min(c0 + lane % 8 * 4, a.r.columns - 4);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int q = lane / 8; q < what.y; q += 4) sum = add4(sum, part_of(a, what.x, q, c));
+        for (int o = 8; o < 32; o *= 2)
+            sum = add4(sum, make_float4(__shfl_xor_sync(~0u, sum.x, o), __shfl_xor_sync(~0u, sum.y, o),
+                                        __shfl_xor_sync(~0u, sum.z, o), __shfl_xor_sync(~0u, sum.w, o)));
+        const int k = lane / 8;                            // each lane writes one of its four columns
+        write_joined(a, key, c0 + lane % 8 * 4 + k, k == 0 ? sum.x : k == 1 ? sum.y : k == 2 ? sum.z : sum.w);
     }
 }
 
@@ -708,7 +892,8 @@ cudaError_t lookup(const q8_embedding& e, const uint16_t* table, void* out, int6
     constexpr int64_t kMost = 1 << 20;
     if (e.dim % 8 == 0 && on16(table) && on16(out) && (e.tokens == 1 || out_stride * sizeof(T) % 16 == 0)) {
         const int64_t tiles = (e.tokens * (e.dim / 8) + kTile * kRowThreads - 1) / (kTile * kRowThreads);
-        lookup_kernel<T><<<static_cast<int>(std::min(kMost, tiles)), kRowThreads, 0, st>>>(e, table, static_cast<T*>(out), out_stride);
+        const auto k = e.tokens * e.dim * int64_t(sizeof(T)) > kStreamBytes ? lookup_kernel<T, true> : lookup_kernel<T, false>;
+        k<<<static_cast<int>(std::min(kMost, tiles)), kRowThreads, 0, st>>>(e, table, static_cast<T*>(out), out_stride);
     } else {
         const int64_t warps = e.tokens * ((e.dim + 255) / 256);
         lookup_odd_kernel<T><<<static_cast<int>(std::min(kMost, (warps + 7) / 8)), kRowThreads, 0, st>>>(e, table, static_cast<T*>(out), out_stride);
@@ -755,14 +940,15 @@ cudaError_t clusters_at_once(int* out)
 }
 
 // The kernel after another one of the same call (wait_for_previous).
-cudaError_t launch_after(void (*kernel)(SumArgs), dim3 grid, int shared, cudaStream_t st, const SumArgs& a)
+template <typename Args>
+cudaError_t launch_after(void (*kernel)(Args), int64_t grid, int threads, int shared, cudaStream_t st, const Args& a)
 {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = shared;
     cfg.stream = st;
     cfg.attrs = &attr;
@@ -795,6 +981,8 @@ cudaError_t prepare_embed()
 {
     int n = 0;
     cudaError_t e = clusters_at_once(&n);
+    for (const void* k : {reinterpret_cast<const void*>(count_kernel), reinterpret_cast<const void*>(place_kernel)})
+        if (e == cudaSuccess) e = persistent_grid(k, kSortThreads, kSortShared, &n);
     for (bool f32 : {false, true})
         for (bool vec : {false, true}) {
             const SumShape s = sum_shape(f32, vec);
@@ -816,8 +1004,10 @@ cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64
     const int size = e.dtype == Q8_F32 ? 4 : 2;
     const bool vec = e.dim % 8 == 0 && on16(dtable) && on16(dout) && (e.tokens == 1 || dout_stride * size % 16 == 0);
     const SumShape sum = sum_shape(size == 4, vec);
-    int clusters = 0, joins = 0;
+    int clusters = 0, sorters = 0, joins = 0;
     cudaError_t err = clusters_at_once(&clusters);
+    for (const void* k : {reinterpret_cast<const void*>(count_kernel), reinterpret_cast<const void*>(place_kernel)})
+        if (err == cudaSuccess) err = persistent_grid(k, kSortThreads, kSortShared, &sorters);
     if (err == cudaSuccess) err = persistent_grid(reinterpret_cast<const void*>(sum.kernel), kRowThreads, sum.shared, &joins);
     if (err == cudaSuccess) err = persistent_grid(reinterpret_cast<const void*>(join_kernel), kRowThreads, 0, &joins);
     if (err != cudaSuccess) return err;
@@ -827,18 +1017,34 @@ cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64
     o.e = e;
     o.r = room;
     o.dtable = dtable;
+    o.clear = !accumulate;
+    o.note = !accumulate && e.tokens <= kClusterTokens;
     int bits = 1;
     while (e.vocab >> bits) ++bits;            // vocab itself is the key of ids outside the table
     o.passes = (bits + kDigitBits - 1) / kDigitBits;
     o.digit = (bits + o.passes - 1) / o.passes;
-    // as many rows as are written while the tokens are sorted
-    const double sort_us = kSortUs + kSortTokenUs * static_cast<double>(e.tokens);
-    const int64_t rows = static_cast<int64_t>(sort_us * kFillBytesUs / (2.0 * static_cast<double>(e.dim)));
-    o.fill = accumulate ? 0 : std::min(e.vocab, rows);
-    const int ctas = accumulate ? kCluster : std::max(2, clusters) * kCluster;
-    cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t cfg = order_config(&attr, ctas, st);
-    if ((err = cudaLaunchKernelEx(&cfg, order_kernel, o)) != cudaSuccess) return err;
+    if (e.tokens <= kClusterTokens) {
+        // as many rows as are written while the tokens are sorted
+        const double sort_us = kSortUs + kSortTokenUs * static_cast<double>(e.tokens);
+        const int64_t rows = static_cast<int64_t>(sort_us * kFillBytesUs / (2.0 * static_cast<double>(e.dim)));
+        o.fill = accumulate ? 0 : std::min(e.vocab, rows);
+        const int ctas = accumulate ? kCluster : std::max(2, clusters) * kCluster;
+        cudaLaunchAttribute attr{};
+        const cudaLaunchConfig_t cfg = order_config(&attr, ctas, st);
+        if ((err = cudaLaunchKernelEx(&cfg, order_kernel, o)) != cudaSuccess) return err;
+    } else {
+        sorters = std::min(sorters, kMaxSorters);
+        for (o.pass = 0; o.pass < o.passes; ++o.pass) {
+            if (o.pass == 0) {
+                count_kernel<<<sorters, kSortThreads, kSortShared, st>>>(o);
+                err = cudaGetLastError();
+            } else {
+                err = launch_after(count_kernel, sorters, kSortThreads, kSortShared, st, o);
+            }
+            if (err == cudaSuccess) err = launch_after(place_kernel, sorters, kSortThreads, kSortShared, st, o);
+            if (err != cudaSuccess) return err;
+        }
+    }
 
     SumArgs s{};
     s.e = e;
@@ -852,11 +1058,13 @@ cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64
     const int64_t each = kRowThreads / s.group;
     s.sums = (room.pieces + each - 1) / each * s.tiles;
     s.filled = o.fill;
-    s.fill_rows = std::max<int64_t>(1, kFillBytes / 2 / e.dim);
-    const int64_t grid = s.sums + (accumulate ? 0 : (e.vocab - o.fill + s.fill_rows - 1) / s.fill_rows);
-    if (grid > std::numeric_limits<int32_t>::max()) return cudaErrorInvalidConfiguration;
-    if ((err = launch_after(sum.kernel, dim3(static_cast<unsigned>(grid)), sum.shared, st, s)) != cudaSuccess) return err;
-    return launch_after(join_kernel, dim3(static_cast<unsigned>(joins / 2)), 0, st, s);
+    s.fill_rows = std::max<int64_t>(1, std::min<int64_t>(kRowThreads, kFillBytes / 2 / e.dim));
+    s.joins = joins;
+    s.late = !accumulate && !o.note;
+    const int64_t fills = accumulate ? 0 : (e.vocab - o.fill + s.fill_rows - 1) / s.fill_rows;
+    if (s.sums + fills > std::numeric_limits<int32_t>::max()) return cudaErrorInvalidConfiguration;
+    if ((err = launch_after(sum.kernel, s.sums + (s.late ? 0 : fills), kRowThreads, sum.shared, st, s)) != cudaSuccess) return err;
+    return launch_after(join_kernel, joins + (s.late ? fills : 0), kRowThreads, 0, st, s);
 }
 
 }  // namespace q8
