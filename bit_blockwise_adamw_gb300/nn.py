@@ -2,9 +2,9 @@
 (include/q8train.h): what comes before the optimizers of
 bit_blockwise_adamw_gb300.optim in a step.
 
-All of them run on CUDA in bf16 (the norms' residual stream and the loss's
-logits also in float32), on the current stream, and accept any leading
-dimensions.  A module's parameters are contiguous bf16 tensors, as the
+All of them run on CUDA in bf16 (the norms' residual stream, the embedding's
+output and the loss's logits also in float32), on the current stream, and accept
+any leading dimensions.  A module's parameters are contiguous bf16 tensors, as the
 optimizers want them.
 """
 import torch
@@ -130,6 +130,45 @@ def distill_topk(logits, teacher_ids, teacher_logits, labels=None, temperature=1
     loss = _DistillTopK.apply(_flat(logits), ids, teacher, None if labels is None else labels.reshape(-1).contiguous(),
                               float(temperature), float(kd_weight), float(ce_weight), torch.is_grad_enabled())
     return loss.view(rows)
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, weight, scale, dtype):
+        out = torch.empty(ids.shape[0], weight.shape[1], dtype=dtype, device=weight.device)
+        B.q8_embedding_forward(ids, weight, out, scale)
+        ctx.save_for_backward(ids)
+        ctx.shape, ctx.scale = weight.shape, scale
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        ids, = ctx.saved_tensors
+        dw = torch.empty(ctx.shape, dtype=torch.bfloat16, device=dout.device)
+        B.q8_embedding_backward(ids, _flat(dout), dw, ctx.scale)
+        return None, dw, None, None
+
+
+def embedding(ids, weight, scale=1.0, dtype=torch.bfloat16):
+    """scale * weight[ids] in bf16 or float32, differentiable in weight: ids
+    outside the table (-100 and the like) are no tokens, their rows are zeros.
+    The same ids and gradients give the same bits."""
+    return _Embedding.apply(ids.reshape(-1).contiguous(), weight, float(scale), dtype).view(*ids.shape, weight.shape[1])
+
+
+class Embedding(nn.Module):
+    """The token embedding, its rows scaled (by the root of the width, where a
+    model does so)."""
+
+    def __init__(self, vocab, dim, scale=1.0, dtype=torch.bfloat16, std=0.02, device=None):
+        super().__init__()
+        self.weight = nn.Parameter(torch.empty(vocab, dim, dtype=torch.bfloat16, device=device))
+        self.scale, self.dtype = scale, dtype
+        nn.init.normal_(self.weight, std=std)
+
+    def forward(self, ids):
+        return embedding(ids, self.weight, self.scale, self.dtype)
 
 
 class GatedFeedForward(nn.Module):

@@ -12,6 +12,10 @@ continues bit for bit.
 The descriptor table a step passes to the library is built once per group
 (state pointers do not move); each step only refreshes its param and grad
 pointers.
+
+max_grad_norm clips the gradients of all groups together before the update, in
+place (clip_grad_norm_), without a synchronisation; `grad_norm` is then the last
+step's norm before clipping, a tensor on the device.
 """
 import numpy as np
 import torch
@@ -33,6 +37,24 @@ def _check_param(p):
     if g.dtype != torch.bfloat16 or not g.is_contiguous() or g.shape != p.shape or g.device != p.device:
         raise ValueError("gradients must be contiguous bf16 tensors shaped like their parameters")
     return g
+
+
+def clip_grad_norm_(parameters, max_norm):
+    """Scales the gradients of the parameters that have one by min(1, max_norm /
+    (norm + 1e-6)), in place, and returns norm, the 2-norm of all of them
+    together: a float32 tensor on their device, with which nothing has
+    synchronised yet.  Gradients are contiguous bf16 or float32 CUDA tensors of
+    one device.  max_norm infinite: the norm alone."""
+    params = [parameters] if torch.is_tensor(parameters) else parameters
+    grads = [p.grad for p in params if p.grad is not None]
+    if not grads:
+        return torch.zeros(())
+    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+    if max_norm == float("inf"):
+        B.q8_grad_norm(grads, norm)
+    else:
+        B.q8_clip_grads(grads, max_norm, norm)
+    return norm
 
 
 class _Table:
@@ -63,8 +85,11 @@ class _FrontEnd(torch.optim.Optimizer):
     casts floating-point state to the parameter's dtype on load, which would
     turn uint8 codes and float32 absmax into bf16)."""
 
-    def __init__(self, params, defaults):
+    def __init__(self, params, defaults, max_grad_norm=None):
+        if max_grad_norm is not None and not max_grad_norm >= 0:
+            raise ValueError("max_grad_norm must be >= 0")
         super().__init__(params, defaults)
+        self.max_grad_norm, self.grad_norm = max_grad_norm, None
         self._next_offset = 0
         self._tables = {}
         # the library's one-time per-device set-up (tables, launch
@@ -107,6 +132,8 @@ class _FrontEnd(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        if self.max_grad_norm is not None:
+            self.grad_norm = clip_grad_norm_([p for g in self.param_groups for p in g["params"]], self.max_grad_norm)
         for gi, group in enumerate(self.param_groups):
             params = [p for p in group["params"] if p.grad is not None]
             if not params:
@@ -143,9 +170,9 @@ class AdamW8bitSR(_Q8Optimizer):
     on rare parameters, never in the state."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, seed=0,
-                 stochastic_rounding=True, exact=False):
+                 stochastic_rounding=True, exact=False, max_grad_norm=None):
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, seed=seed,
-                                      sr=int(stochastic_rounding), exact=int(exact)))
+                                      sr=int(stochastic_rounding), exact=int(exact)), max_grad_norm)
 
     def _run(self, group, arr):
         b1, b2 = group["betas"]
@@ -158,9 +185,10 @@ class Momentum8bitSR(_Q8Optimizer):
     """SGD with momentum, 8-bit blockwise momentum buffer, SR bf16 params."""
     moments = 1
 
-    def __init__(self, params, lr=1e-2, momentum=0.9, weight_decay=0.0, seed=0, stochastic_rounding=True):
+    def __init__(self, params, lr=1e-2, momentum=0.9, weight_decay=0.0, seed=0, stochastic_rounding=True,
+                 max_grad_norm=None):
         super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay, seed=seed,
-                                      sr=int(stochastic_rounding)))
+                                      sr=int(stochastic_rounding)), max_grad_norm)
 
     def _run(self, group, arr):
         B.momentum8bit_sr_step(arr, B.momentum_hparams(lr=group["lr"], momentum=group["momentum"],
@@ -172,9 +200,10 @@ class Lion8bitSR(_Q8Optimizer):
     """Lion with an 8-bit blockwise momentum, SR bf16 params."""
     moments = 1
 
-    def __init__(self, params, lr=1e-4, betas=(0.9, 0.99), weight_decay=0.0, seed=0, stochastic_rounding=True):
+    def __init__(self, params, lr=1e-4, betas=(0.9, 0.99), weight_decay=0.0, seed=0, stochastic_rounding=True,
+                 max_grad_norm=None):
         super().__init__(params, dict(lr=lr, betas=betas, weight_decay=weight_decay, seed=seed,
-                                      sr=int(stochastic_rounding)))
+                                      sr=int(stochastic_rounding)), max_grad_norm)
 
     def _run(self, group, arr):
         b1, b2 = group["betas"]
@@ -189,9 +218,9 @@ class AdamWBF16SR(_FrontEnd):
     _struct = (B._Tensor16, _T16_FIELDS)
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, seed=0,
-                 stochastic_rounding=True, exact=False):
+                 stochastic_rounding=True, exact=False, max_grad_norm=None):
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, seed=seed,
-                                      sr=int(stochastic_rounding), exact=int(exact)))
+                                      sr=int(stochastic_rounding), exact=int(exact)), max_grad_norm)
 
     def _row(self, p):
         _check_param(p)

@@ -5,8 +5,8 @@ optimizer: every operator of the training step as it would be used.
 
 Each step embeds the last tokens of a context, runs blocks of norm, gated
 feed-forward product and gated residual, compares the logits with a fixed
-teacher's sixteen largest (and, in part, with the next token), and steps
-AdamW8bitSR on the bf16 parameters.
+teacher's sixteen largest (and, in part, with the next token), clips the
+gradients' norm and steps AdamW8bitSR on the bf16 parameters.
 """
 import argparse
 import os
@@ -25,7 +25,7 @@ class Student(nn.Module):
     def __init__(self, vocab, dim, d_ff, blocks, context, device):
         super().__init__()
         kw = dict(dtype=torch.bfloat16, device=device)
-        self.embed = nn.Parameter(torch.randn(vocab, dim, device=device).mul_(0.5).bfloat16())
+        self.embed = q8nn.Embedding(vocab, dim, std=0.5, device=device)
         self.mix = nn.Linear(context * dim, dim, bias=False, **kw)
         self.first = q8nn.BlockNorm(dim, post=None, gate=False, device=device)
         self.ff = nn.ModuleList([q8nn.GatedFeedForward(dim, d_ff, device=device) for _ in range(blocks)])
@@ -34,7 +34,7 @@ class Student(nn.Module):
 
     def forward(self, tokens):
         r, z = self.first(torch.zeros(*tokens.shape[:-1], self.head.in_features, dtype=torch.bfloat16, device=tokens.device),
-                          self.mix(self.embed[tokens].flatten(-2)))
+                          self.mix(self.embed(tokens).flatten(-2)))
         for ff, norm in zip(self.ff, self.norm):
             r, z = norm(r, ff(z))
         return self.head(z)
@@ -48,7 +48,7 @@ def train(steps=150, batch=512, vocab=2003, dim=256, d_ff=704, blocks=3, context
         key = torch.randn(vocab, 64, device=device)
         mix = torch.randn(context * 64, 256, device=device) / 16
         out = torch.randn(256, vocab, device=device) / 4
-    opt = AdamW8bitSR(student.parameters(), lr=lr, weight_decay=0.01, seed=seed)
+    opt = AdamW8bitSR(student.parameters(), lr=lr, weight_decay=0.01, seed=seed, max_grad_norm=1.0)
     losses = []
     for _ in range(steps):
         tokens = torch.randint(0, vocab // 20, (batch, context), device=device)
