@@ -115,24 +115,68 @@ __global__ void __launch_bounds__(kRowThreads) lookup_kernel(q8_embedding e, con
     }
 }
 
-// Other rows, element by element: a warp for 256 columns of one row.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) lookup_odd_kernel(q8_embedding e, const uint16_t* table, T* out, int64_t out_stride)
+// Eight bf16 elements, `off` bytes into two 16-byte vectors.
+__device__ __forceinline__ Eight values_across(uint4 a, uint4 b, uint32_t off)
 {
-    const int lane = threadIdx.x % 32;
-    const int64_t parts = (e.dim + 255) / 256, total = e.tokens * parts;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + threadIdx.x / 32; i < total;
-         i += static_cast<int64_t>(gridDim.x) * (kRowThreads / 32)) {
-        const int64_t t = i / parts, id = e.ids[t];
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8)
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    if (off & 4)
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    if (off & 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], w[i + 1], 0x5432);
+    return Eight{{bf16x2(w[0]), bf16x2(w[1]), bf16x2(w[2]), bf16x2(w[3])}};
+}
+
+// Other rows: `group` threads for each, in vectors that start on 16 bytes of the
+// output and lie in two of the table's; a row's first and last elements one by
+// one.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) lookup_odd_kernel(q8_embedding e, const uint16_t* table, T* out, int64_t out_stride, int group)
+{
+    constexpr int kPair = 2;                   // vectors of a thread in flight
+    const int x = threadIdx.x % group, rows = kRowThreads / group;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / group; t < e.tokens; t += static_cast<int64_t>(gridDim.x) * rows) {
+        const int64_t id = e.ids[t];
         const bool known = id >= 0 && id < e.vocab;
-        const int64_t c0 = (i - t * parts) * 256 + lane;
+        const bool inside = id > 0 && id < e.vocab - 1;    // neighbours on both sides: whole vectors may be read
+        T* to = out + t * out_stride;
         const uint16_t* row = table + (known ? id : 0) * e.dim;
-        float x[8];
+        const int64_t lead = min(e.dim, static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(to) % 16) % 16 / sizeof(T)));
+        const int64_t vectors = (e.dim - lead) / 8, tail = lead + vectors * 8 + x;
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + lead) % 16);
+        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row + lead) - off);
+        for (int64_t v0 = x; v0 < vectors; v0 += kPair * group) {
+            uint4 a[kPair], b[kPair];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = known && c0 + j * 32 < e.dim ? load1(row + c0 + j * 32) : 0.0f;
+            for (int j = 0; j < kPair; ++j) {
+                const int64_t v = v0 + j * group;
+                a[j] = b[j] = make_uint4(0, 0, 0, 0);
+                if (v < vectors && inside) {
+                    a[j] = from[v];
+                    if (off) b[j] = from[v + 1];
+                } else if (v < vectors && known) {
+                    uint16_t w[16] = {};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j * 32 < e.dim) store1(out + t * out_stride + c0 + j * 32, known ? __fmul_rn(e.scale, x[j]) : 0.0f);
+                    for (int k = 0; k < 8; ++k) w[k] = row[lead + v * 8 + k];
+                    a[j] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kPair; ++j) {
+                const int64_t v = v0 + j * group;
+                if (v >= vectors) break;
+                Eight y = values_across(a[j], b[j], inside ? off : 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y.x[k] = __fmul2_rn(y.x[k], splat(e.scale));
+                write8(to + lead + v * 8, y);
+            }
+        }
+        if (x < lead) store1(to + x, known ? __fmul_rn(e.scale, load1(row + x)) : 0.0f);
+        if (tail < e.dim) store1(to + tail, known ? __fmul_rn(e.scale, load1(row + tail)) : 0.0f);
     }
 }
 
@@ -895,8 +939,10 @@ cudaError_t lookup(const q8_embedding& e, const uint16_t* table, void* out, int6
         const auto k = e.tokens * e.dim * int64_t(sizeof(T)) > kStreamBytes ? lookup_kernel<T, true> : lookup_kernel<T, false>;
         k<<<static_cast<int>(std::min(kMost, tiles)), kRowThreads, 0, st>>>(e, table, static_cast<T*>(out), out_stride);
     } else {
-        const int64_t warps = e.tokens * ((e.dim + 255) / 256);
-        lookup_odd_kernel<T><<<static_cast<int>(std::min(kMost, (warps + 7) / 8)), kRowThreads, 0, st>>>(e, table, static_cast<T*>(out), out_stride);
+        int group = 8;                         // the first and last elements of a row: seven at most
+        while (group < kRowThreads && group * 16 < e.dim) group *= 2;
+        const int64_t rows = kRowThreads / group;
+        lookup_odd_kernel<T><<<static_cast<int>(std::min(kMost, (e.tokens + rows - 1) / rows)), kRowThreads, 0, st>>>(e, table, static_cast<T*>(out), out_stride, group);
     }
     return cudaGetLastError();
 }
