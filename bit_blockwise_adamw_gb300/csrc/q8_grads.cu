@@ -7,18 +7,20 @@
 // A list travels as kernel parameters, kMaxGrads tensors to a launch.  Each
 // tensor is cut into chunks of 32 KB that start on 16 bytes (the few
 // elements before the first and behind the last whole vector of eight go one by
-// one).  Each CTA adds up its chunks and leaves one sum of squares in the
-// workspace, in double; whoever needs the norm adds these up in one fixed order,
-// without double arithmetic.  Clipping reads the gradients a second time, from
-// the end backwards, so that what was read last, and is still in L2, comes
-// first; the CTAs take the chunks in turn, so that all of them end in that part
-// (40 million float32 to bf16: 59 us; with a run of chunks for each CTA 63 us;
-// 1.56e9 bf16: 1.44 and 1.45 ms).  The norm alone takes them in the same order,
-// so that both calls give the same bits (6.66e9 bf16: 1.81 ms, 7.37 TB/s; runs
-// 1.78 ms).
+// one).  The CTAs take the chunks in turn, and each leaves one sum of squares in
+// the workspace, in double; whoever needs the norm adds these up in one fixed
+// order, without double arithmetic.  Clipping reads the gradients a second time,
+// from the end backwards, so that what was read last, and is still in L2, comes
+// first, a CTA for each chunk.
+//
+// Measured: the norm of 6.66e9 bf16 1.80 ms (7.4 TB/s of reads); clipping of
+// 1.56e9 bf16 1.35 ms (9.35 GB moved, 6.9 TB/s; with as many CTAs as run at
+// once, each with chunks in turn, 1.44 ms), of 40 million float32 to bf16 59 us
+// (L2 has 60 of their 161 MB left; 62 us without).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <limits>
 
 #include "q8_device.cuh"
 #include "q8_internal.h"
@@ -35,7 +37,8 @@ template <typename T> constexpr int kVecs = 16 / sizeof(T);
 template <typename T> constexpr int kChunk = kGradThreads * kVecElems * kVecs<T>;
 constexpr int kChunkBytes = kGradThreads * 128;
 constexpr int kKeepBytes = 60 << 20;                  // of L2's 126 MB
-constexpr int kPerSm = 3;                                  // CTAs of an SM (four: the norm of 6.66e9 1.84 ms instead of 1.78)
+constexpr int kPerSm = 3;                                  // CTAs of an SM that add up (four: 3 % slower)
+constexpr int kClipPerSm = 6;                              // that clip (four: 3 % slower)
 constexpr int kMaxGrads = 768;
 constexpr int kMaxParts = 1024;                            // CTAs of one launch, at most
 
@@ -62,12 +65,13 @@ struct GradArgs {
     float* norm;
     int64_t nchunks;
     float max_norm;
+    int32_t each;              // chunks of a CTA of clip_kernel
     int32_t keep;              // last chunks, which L2 is to keep for the second pass
     int32_t nt;
     int32_t parts_at;          // this launch's place in parts
     int32_t nparts;            // all launches' sums
     uint16_t at[kMaxParts];                // the tensor of each CTA's first chunk
-    uint16_t at_end[kMaxParts];            // and of its first one from the end
+    uint16_t at_end[kMaxParts];            // and of the last chunks, from the end
     int64_t start[ROOM + 1];               // each tensor's first chunk
     Kind kind[ROOM];
     Grad d[ROOM];
@@ -386,22 +390,30 @@ __device__ __forceinline__ void chunk_clip(const T* g, const Grad& d, Kind k, in
 }
 
 template <int ROOM>
-__global__ void __launch_bounds__(kGradThreads, kPerSm) clip_kernel(const __grid_constant__ GradArgs<ROOM> a)
+__global__ void __launch_bounds__(kGradThreads, kClipPerSm) clip_kernel(const __grid_constant__ GradArgs<ROOM> a)
 {
-    int t = a.at_end[blockIdx.x];
+    int64_t c = a.nchunks - 1 - static_cast<int64_t>(blockIdx.x) * a.each;
+    int t = 0;
+    if (blockIdx.x < kMaxParts) {
+        t = a.at_end[blockIdx.x];
+    } else {
+        for (int hi = a.nt; hi - t > 1;) {
+            const int mid = (t + hi) / 2;
+            if (a.start[mid] <= c) t = mid; else hi = mid;
+        }
+    }
     wait_for_previous();
     const float norm = norm_of(a.parts, a.nparts);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
     const float ratio = __fdiv_rn(a.max_norm, __fadd_rn(norm, 1e-6f));
     const float f = ratio >= 1.0f ? 1.0f : ratio;                          // NaN stays NaN
-    for (int64_t c = a.nchunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+    for (const int64_t stop = max(int64_t(0), c + 1 - a.each); c >= stop; --c) {
         while (c < a.start[t]) --t;
         const Grad& d = a.d[t];
         const Kind k = a.kind[t];
-        const int64_t i = c - a.start[t];
         if (f == 1.0f && d.out == d.g) continue;
-        if (k.flags & kF32) chunk_clip(static_cast<const float*>(d.g), d, k, i, f);
-        else chunk_clip(static_cast<const uint16_t*>(d.g), d, k, i, f);
+        if (k.flags & kF32) chunk_clip(static_cast<const float*>(d.g), d, k, c - a.start[t], f);
+        else chunk_clip(static_cast<const uint16_t*>(d.g), d, k, c - a.start[t], f);
     }
 }
 
@@ -448,6 +460,8 @@ cudaError_t run_grads(const q8_grad* list, int count, bool clip, double max_norm
     a.norm = norm;
     a.max_norm = static_cast<float>(std::isinf(max_norm) ? max_norm : std::min(max_norm, static_cast<double>(FLT_MAX)));
     a.nparts = 0;
+    bool in_place = clip;
+    for (int i = 0; i < count && in_place; ++i) in_place = list[i].out == list[i].grad;
     int parts = 0;
     for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
         bool first = true;
@@ -462,13 +476,18 @@ cudaError_t run_grads(const q8_grad* list, int count, bool clip, double max_norm
                 i = count;
             }
             if (a.nchunks == 0) continue;
-            const int ctas = static_cast<int>(std::min<int64_t>(grid, a.nchunks));
+            if (a.nchunks > std::numeric_limits<int32_t>::max()) return cudaErrorInvalidConfiguration;
+            // in place there may be nothing to write, and CTAs that only come to
+            // see that are to be few (1.6e9 bf16 with c = 1: 473 us, the norm alone
+            // 446; with a CTA for each chunk 661)
+            a.each = in_place ? static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(16, a.nchunks / 1024))) : 1;
+            const int ctas = static_cast<int>(pass == 0 ? std::min<int64_t>(grid, a.nchunks) : (a.nchunks + a.each - 1) / a.each);
             for (int b = 0, t = 0; pass == 0 && b < ctas; ++b) {
                 while (b >= a.start[t + 1]) ++t;
                 a.at[b] = static_cast<uint16_t>(t);
             }
-            for (int b = 0, t = a.nt - 1; pass == 1 && b < ctas; ++b) {
-                while (a.nchunks - 1 - b < a.start[t]) --t;
+            for (int b = 0, t = a.nt - 1; pass == 1 && b < ctas && b < kMaxParts; ++b) {
+                while (a.nchunks - 1 - static_cast<int64_t>(b) * a.each < a.start[t]) --t;
                 a.at_end[b] = static_cast<uint16_t>(t);
             }
             if (pass == 0) {
