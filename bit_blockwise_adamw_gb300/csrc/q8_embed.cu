@@ -36,6 +36,7 @@ namespace {
 constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_float(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = float_to_bf16(x); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 
@@ -489,8 +490,16 @@ __device__ __forceinline__ void zero_absent(uint16_t* table, int64_t dim, int64_
             ++r;
             continue;
         }
-        int stop = r + 1;
-        while (stop < end && !(map[stop / 32] >> (stop % 32) & 1)) ++stop;
+        int stop = r;                          // the next bit
+        while (stop < end) {
+            const uint32_t w = map[stop / 32] >> (stop % 32);
+            if (w) {
+                stop += __ffs(w) - 1;
+                break;
+            }
+            stop = (stop / 32 + 1) * 32;
+        }
+        stop = min(stop, end);
         zero_run(table + (first + r) * dim, (stop - r) * dim, lane);
         r = stop;
     }
@@ -678,9 +687,12 @@ struct Columns {
     template <typename U>
     __device__ __forceinline__ Eight read(const U* row) const
     {
-        if constexpr (VEC) {
+        if constexpr (VEC && sizeof(U) == 2) {
             const uint4 w = *reinterpret_cast<const uint4*>(row + first);
             return Eight{{bf16x2(w.x), bf16x2(w.y), bf16x2(w.z), bf16x2(w.w)}};
+        } else if constexpr (VEC) {
+            const float4 u = reinterpret_cast<const float4*>(row + first)[0], w = reinterpret_cast<const float4*>(row + first)[1];
+            return Eight{{make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(w.x, w.y), make_float2(w.z, w.w)}};
         } else {
             Eight v;
 #pragma unroll
@@ -926,6 +938,83 @@ __global__ void __launch_bounds__(kRowThreads) join_kernel(const __grid_constant
     }
 }
 
+// ----------------------------------------------------- gradient of a few tokens
+
+// At most kFewTokens of them, one launch, no sort: the ids are compared with one
+// another.  A CTA for each token and 256 columns: unless its id came before, the
+// CTA's warps take the rows of that id in turn, and their sums are added.
+// Further CTAs write the zeros.
+constexpr int kFewTokens = kRowThreads;        // a thread for each
+constexpr int kFewColumns = 256;
+constexpr int kFewRows = 512;                  // of the table, of a CTA that writes zeros, at most
+
+struct FewArgs {
+    q8_embedding e;
+    const void* dout;
+    int64_t stride;
+    uint16_t* dtable;
+    int64_t sums, fill_rows;
+    int32_t tiles, accumulate;
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) few_kernel(const __grid_constant__ FewArgs a)
+{
+    constexpr int kWarps = kRowThreads / 32;
+    __shared__ __align__(16) float sums[kWarps][kFewColumns];
+    __shared__ uint32_t map[kFewRows / 32], same[kWarps];
+    __shared__ int list[kFewTokens];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    int64_t id = tid < a.e.tokens ? a.e.ids[tid] : -1;
+    if (id >= a.e.vocab) id = -1;
+    if (blockIdx.x >= a.sums) {
+        const int64_t first = (blockIdx.x - a.sums) * a.fill_rows;
+        const int rows = static_cast<int>(min(a.fill_rows, a.e.vocab - first));
+        for (int i = tid; i < (rows + 31) / 32; i += kRowThreads) map[i] = 0;
+        __syncthreads();
+        if (id >= first && id < first + rows) atomicOr(&map[(id - first) / 32], 1u << ((id - first) % 32));
+        __syncthreads();
+        zero_absent(a.dtable, a.e.dim, first, rows * warp / kWarps, rows * (warp + 1) / kWarps, map, lane);
+        return;
+    }
+    const int token = static_cast<int>(blockIdx.x / a.tiles);
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x % a.tiles) * kFewColumns, mine = a.e.ids[token];
+    if (mine < 0 || mine >= a.e.vocab) return;
+    const uint32_t m = __ballot_sync(~0u, id == mine);
+    if (lane == 0) same[warp] = m;
+    __syncthreads();
+    int before = 0, count = 0;                 // tokens of this id in the warps before this one, and in all
+    bool first = true;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? __popc(same[w]) : 0;
+        count += __popc(same[w]);
+        first = first && !(w < token / 32 ? same[w] : w == token / 32 ? same[w] & ((1u << (token % 32)) - 1) : 0);
+    }
+    if (!first) return;
+    if (id == mine) list[before + __popc(m & ((1u << lane) - 1))] = tid;
+    __syncthreads();
+    const Columns<T, VEC> cols{c0 + lane * (VEC ? 8 : sizeof(T) == 2 ? 2 : 1), a.e.dim, 32};
+    Eight sum{};
+    if (cols.first < a.e.dim) {
+#pragma unroll 4
+        for (int i = warp; i < count; i += kWarps) {
+            const Eight x = cols.read(static_cast<const T*>(a.dout) + list[i] * a.stride);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum.x[k] = __fadd2_rn(sum.x[k], x.x[k]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[warp][cols.column(j) - c0] = j % 2 ? sum.x[j / 2].y : sum.x[j / 2].x;
+    __syncthreads();
+    const int64_t c = c0 + tid;
+    if (c >= a.e.dim) return;
+    float x = 0.0f;
+    for (int w = 0; w < min(kWarps, count); ++w) x = __fadd_rn(x, sums[w][tid]);
+    uint16_t* to = a.dtable + mine * a.e.dim + c;
+    store1(to, a.accumulate ? __fmaf_rn(a.e.scale, x, load1(to)) : __fmul_rn(a.e.scale, x));
+}
+
 // ------------------------------------------------------------------------- host
 
 bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -1021,6 +1110,33 @@ SumShape sum_shape(bool f32, bool vec)
                : (vec ? sum_shape<uint16_t, true>() : sum_shape<uint16_t, false>());
 }
 
+using FewKernel = void (*)(FewArgs);
+
+FewKernel few_kernel_of(bool f32, bool vec)
+{
+    return f32 ? (vec ? few_kernel<float, true> : few_kernel<float, false>)
+               : (vec ? few_kernel<uint16_t, true> : few_kernel<uint16_t, false>);
+}
+
+cudaError_t launch_few(const q8_embedding& e, const void* dout, int64_t dout_stride, uint16_t* dtable, bool accumulate, bool vec,
+                       cudaStream_t st)
+{
+    FewArgs a{};
+    a.e = e;
+    a.dout = dout;
+    a.stride = dout_stride;
+    a.dtable = dtable;
+    a.accumulate = accumulate;
+    const int64_t tiles = (e.dim + kFewColumns - 1) / kFewColumns;
+    a.tiles = static_cast<int32_t>(tiles);
+    a.sums = e.tokens * tiles;
+    a.fill_rows = std::max<int64_t>(1, std::min<int64_t>(kFewRows, kFillBytes / 2 / e.dim));
+    const int64_t grid = a.sums + (accumulate ? 0 : (e.vocab + a.fill_rows - 1) / a.fill_rows);
+    if (grid > std::numeric_limits<int32_t>::max()) return cudaErrorInvalidConfiguration;
+    few_kernel_of(e.dtype == Q8_F32, vec)<<<static_cast<unsigned>(grid), kRowThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t prepare_embed()
@@ -1029,9 +1145,14 @@ cudaError_t prepare_embed()
     cudaError_t e = clusters_at_once(&n);
     for (const void* k : {reinterpret_cast<const void*>(count_kernel), reinterpret_cast<const void*>(place_kernel)})
         if (e == cudaSuccess) e = persistent_grid(k, kSortThreads, kSortShared, &n);
+    for (const void* k : {reinterpret_cast<const void*>(lookup_kernel<uint16_t, false>), reinterpret_cast<const void*>(lookup_kernel<uint16_t, true>),
+                          reinterpret_cast<const void*>(lookup_kernel<float, false>), reinterpret_cast<const void*>(lookup_kernel<float, true>),
+                          reinterpret_cast<const void*>(lookup_odd_kernel<uint16_t>), reinterpret_cast<const void*>(lookup_odd_kernel<float>)})
+        if (e == cudaSuccess) e = persistent_grid(k, kRowThreads, 0, &n);
     for (bool f32 : {false, true})
         for (bool vec : {false, true}) {
             const SumShape s = sum_shape(f32, vec);
+            if (e == cudaSuccess) e = persistent_grid(reinterpret_cast<const void*>(few_kernel_of(f32, vec)), kRowThreads, 0, &n);
             if (e == cudaSuccess) e = persistent_grid(reinterpret_cast<const void*>(s.kernel), kRowThreads, s.shared, &n);
         }
     return e == cudaSuccess ? persistent_grid(reinterpret_cast<const void*>(join_kernel), kRowThreads, 0, &n) : e;
@@ -1042,13 +1163,14 @@ cudaError_t launch_embed_forward(const q8_embedding& e, const uint16_t* table, v
     return e.dtype == Q8_F32 ? lookup<float>(e, table, out, out_stride, st) : lookup<uint16_t>(e, table, out, out_stride, st);
 }
 
-int64_t embed_workspace(const q8_embedding& e) { return e.tokens == 0 ? 0 : room_of(e, nullptr).bytes; }
+int64_t embed_workspace(const q8_embedding& e) { return e.tokens <= kFewTokens ? 0 : room_of(e, nullptr).bytes; }
 
 cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64_t dout_stride, uint16_t* dtable,
                                   bool accumulate, void* workspace, cudaStream_t st)
 {
     const int size = e.dtype == Q8_F32 ? 4 : 2;
     const bool vec = e.dim % 8 == 0 && on16(dtable) && on16(dout) && (e.tokens == 1 || dout_stride * size % 16 == 0);
+    if (e.tokens <= kFewTokens) return launch_few(e, dout, dout_stride, dtable, accumulate, vec, st);
     const SumShape sum = sum_shape(size == 4, vec);
     int clusters = 0, sorters = 0, joins = 0;
     cudaError_t err = clusters_at_once(&clusters);

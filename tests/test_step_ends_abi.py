@@ -50,7 +50,6 @@ def test_embedding_refuses_its_other_arguments(lib):
     assert forward(out=0x30001) == ALIGN
     assert forward(e=f, out=0x30002) == ALIGN
     assert forward(stride=63) == SIZE
-    need = lib.q8_embedding_workspace(e)
     back = lambda e=e, dout=0x30000, stride=64, dtable=0x20000, acc=0, ws=0x40000, size=1 << 40: \
         lib.q8_embedding_backward(e, dout, stride, dtable, acc, ws, size, None)
     assert back(e=None) == NULL
@@ -62,10 +61,12 @@ def test_embedding_refuses_its_other_arguments(lib):
     assert back(dtable=0x20001) == ALIGN
     assert back(acc=2) == ARG
     assert back(acc=-1) == ARG
-    if need:
-        assert back(ws=None) == NULL
-        assert back(ws=0x40010) == ALIGN
-        assert back(size=need - 1) == SIZE
+    many = embedding(tokens=5000)
+    need = lib.q8_embedding_workspace(many)
+    assert need > 0
+    assert back(e=many, ws=None) == NULL
+    assert back(e=many, ws=0x40010) == ALIGN
+    assert back(e=many, size=need - 1) == SIZE
     # no tokens: nothing is launched
     assert forward(e=embedding(tokens=0, ids=None), out=None, stride=0) == 0
     assert back(e=embedding(tokens=0, ids=None), dout=None, acc=1) == 0
