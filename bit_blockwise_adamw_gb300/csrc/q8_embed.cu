@@ -795,15 +795,20 @@ __global__ void __launch_bounds__(kRowThreads, 3) sum_kernel(const __grid_consta
     const int known = __popc(__ballot_sync(~0u, key_of(here) < vocab)) + __popc(__ballot_sync(~0u, key_of(behind) < vocab));
     const int count = min(stop, known) - skip;             // ids outside the table come last
     if (count <= 0) return;
-    const auto key_at = [&](int i) { return __shfl_sync(~0u, i + skip < P ? key_of(here) : key_of(behind), i + skip < P ? i + skip : i + skip - P); };
-    const auto token_at = [&](int i) {
-        return __shfl_sync(~0u, static_cast<uint32_t>(i + skip < P ? here : behind), i + skip < P ? i + skip : i + skip - P);
+    // from here on the tokens in the order in which they are added: 0 to 31 and
+    // 32 to 63 of them, one to a lane
+    const auto in_order = [&](uint32_t here_, uint32_t behind_, int i) {
+        const uint32_t x = __shfl_sync(~0u, here_, i & 31), y = __shfl_sync(~0u, behind_, (i - P) & 31);
+        return i < P ? x : y;
     };
-    // bit i: the id of token i (from skip on) ends with it
-    const uint32_t after = __shfl_down_sync(~0u, key_of(here), 1), after2 = __shfl_down_sync(~0u, key_of(behind), 1);
-    const uint32_t m0 = __ballot_sync(~0u, lane < P && key_of(here) != (lane == P - 1 ? first_behind : after));
-    const uint32_t m1 = __ballot_sync(~0u, lane < P && key_of(behind) != after2);
-    const uint64_t ends = ((m0 | static_cast<uint64_t>(m1) << P) >> skip) | uint64_t(1) << (count - 1);
+    const uint32_t key0 = in_order(key_of(here), key_of(behind), lane + skip), key1 = in_order(key_of(here), key_of(behind), lane + skip + 32);
+    const uint32_t token0 = in_order(static_cast<uint32_t>(here), static_cast<uint32_t>(behind), lane + skip);
+    const uint32_t token1 = in_order(static_cast<uint32_t>(here), static_cast<uint32_t>(behind), lane + skip + 32);
+    const auto key_at = [&](int i) { return __shfl_sync(~0u, i < 32 ? key0 : key1, i & 31); };
+    // bit i: the id of token i ends with it, or the piece does
+    const uint32_t next0 = __shfl_down_sync(~0u, key0, 1), next1 = __shfl_down_sync(~0u, key1, 1), start1 = __shfl_sync(~0u, key1, 0);
+    const uint32_t ends0 = __ballot_sync(~0u, lane == count - 1 || key0 != (lane == 31 ? start1 : next0));
+    const uint32_t ends1 = __ballot_sync(~0u, lane + 32 == count - 1 || key1 != next1);
     const uint32_t first_key = key_at(0), last_key = key_at(count - 1);
     const T* dout = static_cast<const T*>(a.dout);
     uint4* mine = ring + threadIdx.x;
@@ -812,12 +817,13 @@ __global__ void __launch_bounds__(kRowThreads, 3) sum_kernel(const __grid_consta
     const Columns<T, VEC> cols{c0 + tid * (VEC ? 8 : sizeof(T) == 2 ? 2 : 1), a.e.dim, a.group};
     const bool on = cols.first < a.e.dim;
     const auto fetch = [&](int i) {                        // kStep rows from i on, one group of copies, be it empty
+        const uint32_t tokens = i < 32 ? token0 : token1;
+        uint4* slot = mine + i % kRing * (kVecs * kRowThreads);
 #pragma unroll
-        for (int j = 0; j < kStep; ++j)
-            if (i + j < count) {
-                const uint32_t t = token_at(i + j);
-                if (on) cols.fetch(mine + (i % kRing + j) * (kVecs * kRowThreads), dout + static_cast<int64_t>(t) * a.stride, t == 0 || t == N - 1);
-            }
+        for (int j = 0; j < kStep; ++j) {
+            const uint32_t t = __shfl_sync(~0u, tokens, (i + j) & 31);
+            if (on && i + j < count) cols.fetch(slot + j * (kVecs * kRowThreads), dout + static_cast<int64_t>(t) * a.stride, t == 0 || t == N - 1);
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
@@ -826,25 +832,33 @@ __global__ void __launch_bounds__(kRowThreads, 3) sum_kernel(const __grid_consta
 #pragma unroll 1
     for (int i = 0; i < count; i += kStep) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing / kStep - 1) : "memory");
-#pragma unroll
-        for (int j = 0; j < kStep; ++j) {
-            if (i + j >= count) break;
+        const uint4* slot = mine + i % kRing * (kVecs * kRowThreads);
+        const uint32_t ends = (i < 32 ? ends0 : ends1) >> (i & 31), tokens = i < 32 ? token0 : token1;
+        const auto add = [&](int j) {
             const T* row = dout;                           // its alignment is all that counts
-            if constexpr (!VEC && sizeof(T) == 2) row += static_cast<int64_t>(token_at(i + j)) * a.stride;
-            if (on) cols.add(sum, mine + (i % kRing + j) * (kVecs * kRowThreads), row);
-            if (!(ends >> (i + j) & 1)) continue;
-            const uint32_t key = key_at(i + j);
-            if (on) {
-                if (key == first_key && from_before) {
-                    cols.write(a.r.parts + (piece * 2) * a.r.columns, sum);
-                    sum = Eight{};
-                    continue;
+            if constexpr (!VEC && sizeof(T) == 2) row += static_cast<int64_t>(__shfl_sync(~0u, tokens, (i + j) & 31)) * a.stride;
+            if (on) cols.add(sum, slot + j * (kVecs * kRowThreads), row);
+        };
+        if (!(ends & ((1u << kStep) - 1))) {               // all of one id, which goes on
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) add(j);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kStep && i + j < count; ++j) {
+                add(j);
+                if (!(ends >> j & 1)) continue;
+                const uint32_t key = key_at(i + j);
+                if (on) {
+                    if (key == first_key && from_before) {
+                        cols.write(a.r.parts + (piece * 2) * a.r.columns, sum);
+                    } else {
+                        if (a.late && blockIdx.x % a.tiles == 0 && tid == 0) a.r.present[key] = 1;
+                        if (i + j == count - 1 && goes_on) cols.write(a.r.parts + (piece * 2 + 1) * a.r.columns, sum);
+                        else cols.write_scaled(a.dtable + static_cast<int64_t>(key) * a.e.dim, sum, a.e.scale, a.accumulate);
+                    }
                 }
-                if (a.late && blockIdx.x % a.tiles == 0 && tid == 0) a.r.present[key] = 1;
-                if (i + j == count - 1 && goes_on) cols.write(a.r.parts + (piece * 2 + 1) * a.r.columns, sum);
-                else cols.write_scaled(a.dtable + static_cast<int64_t>(key) * a.e.dim, sum, a.e.scale, a.accumulate);
+                sum = Eight{};
             }
-            sum = Eight{};
         }
         fetch(i + kRing);
     }
