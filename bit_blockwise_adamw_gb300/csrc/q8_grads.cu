@@ -144,9 +144,9 @@ __device__ __noinline__ double squares_scaled(const T* p, const T* stop)
 }
 
 // A thread's sum of squares: hi + lo in fp32, lo what hi's roundings lost (Knuth's
-// two-sum), and what came out of range for them in double.  This GPU adds 64
-// floats in the time of one double: sums in double alone cost 6 us of a clipping
-// of 8 MB.
+// two-sum), and what came out of range for them in double.  This GPU adds some
+// sixty floats in the time of one double: sums in double alone cost 6 us of a
+// clipping of 8 MB.
 struct Sum {
     float hi = 0.0f, lo = 0.0f;
     double rare = 0.0;

@@ -222,7 +222,8 @@ int q8_distill_topk_backward(const q8_distill_topk* d, const float* stats, void*
  *   dW[v] = scale * (sum of dout[t] over the t with ids[t] = v)  [vocab, dim].
  * An id outside [0, vocab) is no token: its row of out is zeros, and its row of
  * dout is not read.  out and dout have the type dtype.  The sum of a table row
- * is fp32, over the tokens' order in an association that depends on ids alone.
+ * is fp32, over the tokens' order in an association that depends on the ids and
+ * the sizes alone.
  * 0 <= tokens < 2^30, 1 <= vocab < 2^31, 1 <= dim < 2^30, scale finite.
  */
 typedef struct {

@@ -126,7 +126,8 @@ def test_gradient(cuda_device, T, V, D, dtype):
         check_grad(ids, dout, got, scale, base)
 
 
-@pytest.mark.parametrize("T,V,D", [(6000, 5000, 264), (40000, 50257, 72), (70000, 130000, 24), (262144, 50257, 8), (300001, 17, 16)])
+@pytest.mark.parametrize("T,V,D", [(6000, 5000, 264), (40000, 50257, 72), (70000, 130000, 24), (262144, 50257, 8), (300001, 17, 16),
+                                   (1300001, 50257, 8)])
 @pytest.mark.parametrize("kind", ["uniform", "one", "skewed", "padded"])
 def test_gradient_of_many_tokens_is_exact_on_whole_numbers(cuda_device, T, V, D, kind):
     """Sums of small whole numbers are exact in float32 in any order (below
@@ -140,6 +141,29 @@ def test_gradient_of_many_tokens_is_exact_on_whole_numbers(cuda_device, T, V, D,
     total = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, ids[known], dout[known].double())
     assert float(total.abs().max()) < 2 ** 24
     assert torch.equal(got, (total * 0.5).float().to(BF))
+
+
+def test_tens_of_millions_of_tokens(cuda_device):
+    """More rows than a launch has CTAs, more tokens than the sort's CTAs hold at
+    once; whole numbers, so that every result is known exactly."""
+    T, V, D = 34000001, 1000, 9
+    ids = make_ids("padded", T, V, seed=3)
+    ids[:T // 2] = make_ids("uniform", T // 2, V, seed=4)
+    table = torch.randint(-100, 101, (V, D), device="cuda").to(BF)
+    out = torch.empty(T, D, dtype=BF, device="cuda")
+    q8.q8_embedding_forward(ids, table, out, scale=-1.0)
+    for t in torch.arange(T, device="cuda").split(1 << 22):
+        known = (ids[t] >= 0) & (ids[t] < V)
+        assert torch.equal(out[t], torch.where(known[:, None], -table[ids[t].clamp(0, V - 1)], 0.0).to(BF) + 0.0)
+    out.view(torch.int16).random_(0, 2)              # ones and zeros, as bits
+    out = out.view(torch.int16).to(BF)
+    got = torch.full((V, D), float("nan"), dtype=BF, device="cuda")
+    q8.q8_embedding_backward(ids, out, got)
+    total = torch.zeros(V, D, dtype=torch.float64, device="cuda")
+    for t in torch.arange(T, device="cuda").split(1 << 22):
+        known = t[(ids[t] >= 0) & (ids[t] < V)]
+        total.index_add_(0, ids[known], out[known].double())
+    assert float(total.max()) < 2 ** 24 and torch.equal(got, total.float().to(BF))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
