@@ -6,6 +6,7 @@ all work runs in the library's kernels.  A missing library is an error: there
 is no fallback path.
 """
 import ctypes as C
+import importlib.util
 import os
 import struct
 from dataclasses import dataclass
@@ -693,40 +694,32 @@ def q8_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, dtable: torch.T
     _run("q8_embedding_backward", dout, e, dp, ds, gp, int(accumulate), wp, wb, _on(stream, dout))
 
 
+_lists = None
+
+
+def _lists_module():
+    """The CPython module that packs lists of tensors, loaded once."""
+    global _lists
+    if _lists is None:
+        path = _build.lists_module()
+        if not os.path.exists(path):
+            raise RuntimeError("%s is not built; run bit_blockwise_adamw_gb300.build.build()" % path)
+        spec = importlib.util.spec_from_file_location("q8_lists", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _lists = module
+    return _lists
+
+
 class Grads:
     """A list of gradients (and of where their clipped forms go) as the library
     takes it: keep it to pass the same tensors again."""
-    __slots__ = ("bytes", "count", "like", "tensors", "clips")
+    __slots__ = ("bytes", "count", "device", "tensors")
 
     def __init__(self, grads, out=None):
-        self.tensors = (list(grads), None if out is None else list(out))
-        self.clips = out is not None
-        grads, out = self.tensors
-        self.count, self.like = len(grads), grads[0] if grads else None
-        kinds = self._kinds(grads, "gradients")
-        sizes = list(map(torch.Tensor.numel, grads))
-        ptrs = list(map(torch.Tensor.data_ptr, grads))
-        if out is None:
-            outs, okinds = ptrs, kinds
-        else:
-            okinds = self._kinds(out, "out")
-            if list(map(torch.Tensor.numel, out)) != sizes:
-                raise ValueError("out must hold a tensor of each gradient's number of elements")
-            outs = list(map(torch.Tensor.data_ptr, out))
-        pack = _GRAD.pack
-        self.bytes = b"".join(map(pack, ptrs, outs, sizes, kinds, okinds))
-
-    def _kinds(self, tensors, name):
-        """Each tensor's q8_dtype."""
-        try:
-            kinds = [_DTYPES[t.dtype] for t in tensors]
-        except KeyError:
-            raise ValueError("%s must be bfloat16 or float32" % name) from None
-        if not all(map(torch.Tensor.is_contiguous, tensors)):
-            raise ValueError("%s must be contiguous" % name)
-        if tensors and (not self.like.is_cuda or set(map(torch.Tensor.get_device, tensors)) != {self.like.get_device()}):
-            raise ValueError("%s must be CUDA tensors of one device" % name)
-        return kinds
+        grads, out = list(grads), None if out is None else list(out)
+        self.bytes, self.device = (_lists or _lists_module()).pack(grads, out)
+        self.count, self.tensors = len(grads), (grads, out)
 
 
 def pack_grads(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None) -> Grads:
@@ -741,7 +734,7 @@ def _grads_call(fn, grads, norm, workspace, stream, *args):
     np_ = _array(norm, "norm", _F32, norm.shape)
     if norm.numel() != 1:
         raise ValueError("norm must hold one float32")
-    if grads.like is not None and grads.like.get_device() != norm.get_device():
+    if grads.device not in (-1, norm.get_device()):
         raise ValueError("norm must be on the gradients' device")
     need = L.q8_grad_norm_workspace(grads.count)
     wp, wb, keep = _workspace(fn, need, workspace, norm, stream)

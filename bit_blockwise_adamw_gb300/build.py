@@ -3,13 +3,15 @@
 Every translation unit is compiled by nvcc for sm_103a only, in parallel,
 then linked into one shared library that exports the C ABI of
 include/q8adamw.h.  Floating-point contraction is off (--fmad=false): each
-fp32 operation of the step rounds on its own.
+fp32 operation of the step rounds on its own.  Beside it goes a small CPython
+module of the binding (csrc/q8_lists.cpp, g++), for the installed torch.
 """
 import concurrent.futures as cf
 import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +24,31 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--fmad=false",
                      "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                      "-I", INCLUDE, "-I", CSRC]
+
+
+def lists_module():
+    """Path of the CPython module of csrc/q8_lists.cpp, which holds for one version of torch and of Python."""
+    import torch
+    return os.path.join(OUT_DIR, "q8_lists-%s-%s" % (torch.__version__, sysconfig.get_config_var("EXT_SUFFIX").lstrip(".")))
+
+
+def _build_lists(force):
+    import torch
+    src, out = os.path.join(CSRC, "q8_lists.cpp"), lists_module()
+    inputs = [src, os.path.join(INCLUDE, "q8train.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, inputs)):
+        return
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    tmp = out + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], src, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
+    os.replace(tmp, out)
 
 
 def nvcc():
@@ -48,9 +75,10 @@ def _stale():
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile and link the library if any input changed; return its path."""
-    if not force and not _stale():
-        return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
+    if not force and not _stale():
+        _build_lists(False)
+        return LIB
     cc = nvcc()
     flags = NVCC_FLAGS + list(extra_flags)
 
@@ -62,8 +90,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
         return obj, r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 4)) as ex:
+        lists = ex.submit(_build_lists, force)
         results = list(ex.map(compile_one, _sources()))
+        lists.result()
     if verbose:
         for _, log in results:
             if log.strip():

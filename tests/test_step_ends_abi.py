@@ -111,7 +111,7 @@ def test_grads_refuse_their_other_arguments(lib):
     assert clip(limit=float("nan")) == ARG
 
 
-def test_binding_refuses_host_tensors_and_mismatches():
+def test_binding_refuses_host_tensors_and_mismatches(lib):
     ids, w, out = torch.zeros(2, dtype=torch.int64), torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(2, 8, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="table must be"):
         q8.q8_embedding_forward(ids, w, out)
@@ -123,7 +123,17 @@ def test_binding_refuses_host_tensors_and_mismatches():
         q8.pack_grads([w])
     with pytest.raises(ValueError, match="bfloat16 or float32"):
         q8.pack_grads([w.half()])
-    with pytest.raises(ValueError, match="contiguous"):
-        q8.pack_grads([w.t()])
+    for bad in (w.t(), w.float().to_sparse(), torch.zeros(6, device="meta")[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            q8.pack_grads([bad])
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        q8.pack_grads([torch.zeros(6, device="meta")])
+    with pytest.raises(ValueError, match="must be tensors"):
+        q8.pack_grads([None])
+    with pytest.raises(ValueError, match="number of elements"):
+        q8.pack_grads([w], [])
+    with pytest.raises(TypeError):
+        q8.pack_grads(3)
+    assert q8.pack_grads([]).count == 0 and q8.pack_grads(iter([])).bytes == b""
     with pytest.raises(ValueError, match="norm must be"):
         q8.q8_grad_norm([], torch.zeros(1))
