@@ -6,11 +6,13 @@
 // rows that they move.
 //
 // Up to 256 tokens take one launch (few_kernel).  More take three.
-//  1. order_kernel.  One cluster of eight CTAs sorts the tokens by their id
+//  1. rank_kernel, up to 4096 tokens and 64 MB of zeros: each token's place is the
+//     number of those before it by id and order, counted by comparing it with all
+//     of them; other CTAs write the zeros of the table's rows that no token has.
+//     Elsewhere, order_kernel.  One cluster of eight CTAs sorts the tokens by their id
 //     (stable, so that a row's tokens keep their order: least significant digit
 //     first, up to nine bits a pass, counts exchanged through the cluster's
-//     shared memory), while all other CTAs write zeros into the first of the
-//     table's rows that no token has.
+//     shared memory), the other CTAs writing zeros.
 //  2. sum_kernel.  The sorted tokens are cut into pieces of 8 or 32; a group of
 //     warps adds up a piece's rows for its columns, in fp32 registers, and
 //     writes a table row whenever the id changes.  An id of no more tokens than
@@ -24,7 +26,7 @@
 //
 // Measured, bf16, a vocabulary of 50257, tokens as frequent as words are: lookup
 // of 16384 x 4096 32 us (5.8 TB/s), of one row 1.8 us.  Gradient of 16384 x 4096
-// 95 us (546 MB that it cannot do without: 5.7 TB/s), of 262144 x 1024 of which
+// 94 us (546 MB that it cannot do without: 5.8 TB/s), of 262144 x 1024 of which
 // half are padding 150 us (sort 27, sums 100, joins 23), of 24 x 2560 38.3 us (all
 // of it the table's zeros: 6.7 TB/s).
 #include <algorithm>
@@ -272,6 +274,7 @@ struct OrderArgs {
     int32_t pass;              // count_kernel, place_kernel: the one at hand
     int32_t clear, note;       // r.present is cleared; the sort notes there what it meets
     int64_t fill;              // the table's rows [0, fill) get their zeros here
+    int64_t fill_rows;         // rank_kernel: so many to a CTA
 };
 
 __device__ __forceinline__ uint32_t cluster_read(const uint32_t* p, uint32_t rank)
@@ -541,6 +544,60 @@ __device__ void fill_rows(const OrderArgs& a, uint32_t* map, int64_t cta, int64_
 
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Each token's place: the tokens of smaller ids, and those of its own before it.
+// A CTA for 32 tokens, eight lanes for each, all ids in shared memory (added to
+// their rows of 1024, 1024 / 4096 / 8192 tokens 11 / 16 / 30 us, by way of the
+// cluster's sort 17 / 20 / 25).  The zeros of a large table are better written
+// beside the sums, too (1024 x 752 rows of 4336 13 us, by the cluster 18; 385 x
+// 10594 of 3704 26 and 27; 1024 x 50257 of 1024 30 and 27).
+constexpr int kRankTokens = 4096;
+constexpr int64_t kRankZeros = 64 << 20;
+constexpr int kRanked = kRowThreads / 8;       // tokens of a CTA
+constexpr int kRankRows = 512;                 // of the table, of a CTA that writes zeros, at most
+
+__global__ void __launch_bounds__(kRowThreads) rank_kernel(const __grid_constant__ OrderArgs a)
+{
+    extern __shared__ __align__(16) uint32_t shared[];
+    let_next_start();
+    const int tid = threadIdx.x, tokens = static_cast<int>(a.e.tokens);
+    const int ctas = (tokens + kRanked - 1) / kRanked;
+    if (static_cast<int>(blockIdx.x) >= ctas) {
+        constexpr int kWarps = kRowThreads / 32;
+        const int64_t first = (static_cast<int64_t>(blockIdx.x) - ctas) * a.fill_rows;
+        const int rows = static_cast<int>(min(a.fill_rows, a.fill - first)), warp = tid / 32;
+        for (int i = tid; i < (rows + 31) / 32; i += kRowThreads) shared[i] = 0;
+        __syncthreads();
+#pragma unroll 8
+        for (int t = tid; t < tokens; t += kRowThreads) {
+            const uint64_t r = static_cast<uint64_t>(a.e.ids[t]) - static_cast<uint64_t>(first);
+            if (r < static_cast<uint64_t>(rows) && !(static_cast<volatile uint32_t*>(shared)[r / 32] >> (r % 32) & 1)) atomicOr(&shared[r / 32], 1u << (r % 32));
+        }
+        __syncthreads();
+        zero_absent(a.dtable, a.e.dim, first, rows * warp / kWarps, rows * (warp + 1) / kWarps, shared, tid % 32);
+        return;
+    }
+    if (blockIdx.x == 0 && tid < 2) a.r.count[tid] = 0;
+    const int vectors = (tokens + 3) / 4;
+#pragma unroll 8
+    for (int t = tid; t < vectors * 4; t += kRowThreads) {
+        const int64_t id = t < tokens ? a.e.ids[t] : -1;
+        shared[t] = t >= tokens ? ~0u : static_cast<uint32_t>(id >= 0 && id < a.e.vocab ? id : a.e.vocab);
+    }
+    __syncthreads();
+    const int t = blockIdx.x * kRanked + tid / 8;
+    const uint32_t mine = t < tokens ? shared[t] : 0;
+    uint32_t place = 0;
+#pragma unroll 8
+    for (int v = tid % 8; v < vectors; v += 8) {
+        const uint4 x = reinterpret_cast<const uint4*>(shared)[v];
+        const uint32_t below = mine + (v < t / 4);         // equal ones count before this token's own four
+        place += (x.x < below) + (x.y < below) + (x.z < below) + (x.w < below);
+    }
+    if (tid % 8 < t % 4 && t < tokens) place += shared[t / 4 * 4 + tid % 8] == mine;
+    for (int o = 1; o < 8; o *= 2) place += __shfl_xor_sync(~0u, place, o);
+    if (tid % 8 == 0 && t < tokens) a.r.sorted[place] = static_cast<uint64_t>(mine) << 32 | static_cast<uint32_t>(t);
+}
 
 __global__ void __launch_bounds__(kSortThreads) order_kernel(const __grid_constant__ OrderArgs a)
 {
@@ -1173,6 +1230,7 @@ cudaError_t prepare_embed()
 {
     int n = 0;
     cudaError_t e = clusters_at_once(&n);
+    if (e == cudaSuccess) e = persistent_grid(reinterpret_cast<const void*>(rank_kernel), kRowThreads, 0, &n);
     for (const void* k : {reinterpret_cast<const void*>(count_kernel), reinterpret_cast<const void*>(place_kernel)})
         if (e == cudaSuccess) e = persistent_grid(k, kSortThreads, kSortShared, &n);
     for (const void* k : {reinterpret_cast<const void*>(lookup_kernel<uint16_t, false>), reinterpret_cast<const void*>(lookup_kernel<uint16_t, true>),
@@ -1215,13 +1273,21 @@ cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64
     o.e = e;
     o.r = room;
     o.dtable = dtable;
-    o.clear = !accumulate;
     o.note = !accumulate && e.tokens <= kClusterTokens;
+    o.clear = !accumulate;
     int bits = 1;
     while (e.vocab >> bits) ++bits;            // vocab itself is the key of ids outside the table
     o.passes = (bits + kDigitBits - 1) / kDigitBits;
     o.digit = (bits + o.passes - 1) / o.passes;
-    if (e.tokens <= kClusterTokens) {
+    if (e.tokens <= kRankTokens && (accumulate || 2 * e.vocab * e.dim <= kRankZeros)) {
+        o.note = 0;
+        o.fill = accumulate ? 0 : e.vocab;
+        o.fill_rows = std::max<int64_t>(1, std::min<int64_t>(kRankRows, kFillBytes / 2 / e.dim));
+        const int64_t grid = (e.tokens + kRanked - 1) / kRanked + (o.fill + o.fill_rows - 1) / o.fill_rows;
+        const int shared = std::max<int>(static_cast<int>(e.tokens + 3) / 4 * 16, kRankRows / 8);
+        rank_kernel<<<static_cast<unsigned>(grid), kRowThreads, shared, st>>>(o);
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    } else if (e.tokens <= kClusterTokens) {
         // as many rows as are written while the tokens are sorted
         const double sort_us = kSortUs + kSortTokenUs * static_cast<double>(e.tokens);
         const int64_t rows = static_cast<int64_t>(sort_us * kFillBytesUs / (2.0 * static_cast<double>(e.dim)));
@@ -1258,7 +1324,7 @@ cudaError_t launch_embed_backward(const q8_embedding& e, const void* dout, int64
     s.filled = o.fill;
     s.fill_rows = std::max<int64_t>(1, std::min<int64_t>(kRowThreads, kFillBytes / 2 / e.dim));
     s.joins = joins;
-    s.late = !accumulate && !o.note;
+    s.late = !accumulate && e.tokens > kClusterTokens;
     const int64_t fills = accumulate ? 0 : (e.vocab - o.fill + s.fill_rows - 1) / s.fill_rows;
     if (s.sums + fills > std::numeric_limits<int32_t>::max()) return cudaErrorInvalidConfiguration;
     if ((err = launch_after(sum.kernel, s.sums + (s.late ? 0 : fills), kRowThreads, sum.shared, st, s)) != cudaSuccess) return err;

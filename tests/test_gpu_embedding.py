@@ -91,7 +91,8 @@ def check_grad(ids, dout, got, scale, base=None):
 
 
 SIZES = [(1, 1, 1), (1, 50257, 64), (255, 3, 257), (256, 40, 24), (256, 5000, 1031), (3, 7, 8), (33, 10, 5), (257, 1000, 136), (300, 513, 264), (1000, 65537, 33), (2049, 300, 96),
-         (5000, 70000, 40), (777, 2000, 1601), (130, 999, 4104), (19, 64, 9000)]
+         (5000, 70000, 40), (777, 2000, 1601), (130, 999, 4104), (19, 64, 9000),
+         (257, 50257, 712), (1500, 50257, 1000), (4096, 900, 24), (4097, 900, 24), (8193, 40, 520), (32769, 300, 8)]
 KINDS = ["uniform", "one", "skewed", "padded", "outside", "ends", "runs"]
 
 
