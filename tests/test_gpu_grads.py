@@ -57,6 +57,8 @@ LISTS = {
     "chunk edges": [16383, 16384, 16385, 32767, 32768, 32769, 65535, 65537, 131071, 131073],
     "many": [(i * 37) % 5000 + 1 for i in range(1700)],
     "a long one among short ones": [64, 3000001, 64, 1, 2000000],
+    "more chunks than parts": [9000001, 3, 7000003, 16385, 12000001, 5],
+    "several chunks to a CTA": [20000001, 77, 30000005, 4097],
 }
 
 
