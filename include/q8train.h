@@ -252,11 +252,13 @@ int q8_embedding_backward(const q8_embedding* e, const void* dout, int64_t dout_
  * Over a list of `count` gradients g_i (host array), as one flat vector:
  *   norm = sqrt(sum over i, j of g_ij^2)
  *   c = min(1, max_norm / (norm + 1e-6)),  out_ij = c * g_ij.
- * Squares are summed in fp32 over at most 128 elements, scaled by a power of
- * two where they would leave fp32's range, and from there in pairs of fp32 (or
- * double): no norm below 2^128 overflows, none is lost, and beyond the 128
- * terms' roundings norm and c carry less than 16 roundings of fp32 each.  With an infinite gradient the norm is infinite and c is 0
- * (infinite elements then give NaN); with NaN both are NaN and all results are.
+ * Squares are summed in fp32 over at most 64 elements, scaled by a power of
+ * two where they would leave fp32's range, these sums in pairs of fp32 (or
+ * double) and those of the CTAs as whole numbers: no norm below 2^128 overflows,
+ * none is lost, and beyond the 64 terms' roundings the norm carries two roundings
+ * of fp32 and c five, of up to 2^27 tensors and 2^34 elements in all.  With an
+ * infinite gradient the norm is infinite and c is 0 (infinite elements then give
+ * NaN); with NaN both are NaN and all results are.
  * grad and out are contiguous, on their elements' own alignment; out may be
  * grad itself where both have one type, and out_dtype may differ from
  * grad_dtype elsewhere.  Clipping in place with c = 1 writes nothing.
