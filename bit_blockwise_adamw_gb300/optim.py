@@ -44,9 +44,10 @@ def clip_grad_norm_(parameters, max_norm):
     (norm + 1e-6)), in place, and returns norm, the 2-norm of all of them
     together: a float32 tensor on their device, with which nothing has
     synchronised yet.  Gradients are contiguous bf16 or float32 CUDA tensors of
-    one device.  max_norm infinite: the norm alone."""
+    one device; a parameter that comes twice counts once.  max_norm infinite: the
+    norm alone."""
     params = [parameters] if torch.is_tensor(parameters) else parameters
-    grads = [p.grad for p in params if p.grad is not None]
+    grads = [p.grad for p in {id(p): p for p in params}.values() if p.grad is not None]
     if not grads:
         return torch.zeros(())
     norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
