@@ -758,7 +758,8 @@ def q8_grad_norm(grads, norm: torch.Tensor, workspace: Optional[torch.Tensor] = 
 def q8_clip_grads(grads, max_norm: float, norm: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """The gradients times min(1, max_norm / (norm + 1e-6)), in place or into
-    out's tensors (bf16 or float32 each); norm as by q8_grad_norm."""
+    out's tensors (bf16 or float32 each), none of which may share memory with
+    another's gradient or output; norm as by q8_grad_norm."""
     if isinstance(grads, Grads):
         if out is not None:
             raise ValueError("out is part of the packed list")

@@ -1,9 +1,12 @@
 // q8_train_api.cu -- the extern "C" entry points declared in
 // include/q8train.h: argument checks, then the launchers.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "q8_internal.h"
 #include "q8_train.h"
@@ -159,6 +162,49 @@ int check_grads(const q8_grad* list, int count, bool clip)
         if (!g.out) return fail(Q8_ERR_NULL, entry("out is NULL", i));
         if (!aligned(g.out, g.out_dtype == Q8_F32 ? 4 : 2)) return fail(Q8_ERR_ALIGN, entry("out is not aligned to its elements", i));
         if (g.out == g.grad && g.out_dtype != g.grad_dtype) return fail(Q8_ERR_ARG, entry("out over grad must have grad's type", i));
+    }
+    return Q8_OK;
+}
+
+// What clipping writes, in bytes, and the entry that it is of.
+struct Span {
+    uintptr_t begin, end;
+    int entry;
+};
+
+Span span_of(const void* p, int64_t numel, int32_t dtype, int i)
+{
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(p);
+    return {begin, begin + static_cast<uintptr_t>(numel) * (dtype == Q8_F32 ? 4 : 2), i};
+}
+
+// Outputs that overlap one another or a gradient (but their own at the same
+// address) would be read and written by several CTAs in no order.  Outputs that
+// come in the order of their addresses, apart from the gradients, as those of one
+// buffer do, take one look at each; else they are sorted.
+int check_overlaps(const q8_grad* list, int count)
+{
+    try {
+        std::vector<Span> outs;
+        outs.reserve(static_cast<size_t>(count));
+        for (int i = 0; i < count; ++i)
+            if (list[i].numel) outs.push_back(span_of(list[i].out, list[i].numel, list[i].out_dtype, i));
+        if (outs.empty()) return Q8_OK;
+        const auto before = [](const Span& a, const Span& b) { return a.begin != b.begin ? a.begin < b.begin : a.entry < b.entry; };
+        if (!std::is_sorted(outs.begin(), outs.end(), before)) std::sort(outs.begin(), outs.end(), before);
+        for (size_t k = 1; k < outs.size(); ++k)
+            if (outs[k].begin < outs[k - 1].end) return fail(Q8_ERR_ARG, entry("out overlaps another's out", outs[k].entry));
+        for (int i = 0; i < count; ++i) {
+            const q8_grad& g = list[i];
+            if (g.numel == 0 || g.out == g.grad) continue;
+            const Span s = span_of(g.grad, g.numel, g.grad_dtype, i);
+            if (s.end <= outs.front().begin || s.begin >= outs.back().end) continue;
+            // the last output that begins before the gradient ends
+            const auto o = std::partition_point(outs.begin(), outs.end(), [&](const Span& x) { return x.begin < s.end; });
+            if (o != outs.begin() && (o - 1)->end > s.begin) return fail(Q8_ERR_ARG, entry("grad overlaps an out", i));
+        }
+    } catch (const std::bad_alloc&) {
+        return fail(Q8_ERR_SIZE, "no host memory for a list of so many gradients");
     }
     return Q8_OK;
 }
@@ -368,6 +414,7 @@ int q8_clip_grads(const q8_grad* list, int count, double max_norm, float* norm, 
                   int64_t workspace_bytes, q8_stream_t stream)
 {
     int rc = check_grads(list, count, true);
+    if (rc == Q8_OK) rc = check_overlaps(list, count);
     if (rc == Q8_OK && !(max_norm >= 0.0)) rc = fail(Q8_ERR_ARG, "max_norm must be >= 0");
     if (rc == Q8_OK) rc = check_norm_output(norm);
     if (rc == Q8_OK) rc = check_workspace(workspace, workspace_bytes, q8::grads_workspace(count));

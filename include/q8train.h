@@ -261,7 +261,9 @@ int q8_embedding_backward(const q8_embedding* e, const void* dout, int64_t dout_
  * NaN); with NaN both are NaN and all results are.
  * grad and out are contiguous, on their elements' own alignment; out may be
  * grad itself where both have one type, and out_dtype may differ from
- * grad_dtype elsewhere.  Clipping in place with c = 1 writes nothing.
+ * grad_dtype elsewhere.  An out that overlaps another entry's out or grad, or its
+ * own grad in another way, is refused (the same tensor twice, in place): entries
+ * are clipped in no order.  Clipping in place with c = 1 writes nothing.
  * numel 0 entries are skipped.  0 <= count, 0 <= numel < 2^40; max_norm >= 0
  * (it may be infinite: c is then 1 or NaN).
  */
