@@ -15,7 +15,9 @@ pointers.
 
 max_grad_norm clips the gradients of all groups together before the update, in
 place (clip_grad_norm_), without a synchronisation; `grad_norm` is then the last
-step's norm before clipping, a tensor on the device.
+step's norm before clipping, a tensor on the device.  A step that is refused for
+a parameter's or gradient's type, layout or alignment leaves all of them as they
+were.
 """
 import numpy as np
 import torch
@@ -133,13 +135,21 @@ class _FrontEnd(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        if self.max_grad_norm is not None:
-            self.grad_norm = clip_grad_norm_([p for g in self.param_groups for p in g["params"]], self.max_grad_norm)
+        # every group's parameters and gradients are looked at before the first
+        # change of any of them
+        todo = []
         for gi, group in enumerate(self.param_groups):
             params = [p for p in group["params"] if p.grad is not None]
-            if not params:
-                continue
-            arr = self._table(gi, params)
+            if params:
+                todo.append((group, self._table(gi, params)))
+        if self.max_grad_norm is not None:
+            numel = self._struct[1].index("numel")
+            for _, arr in todo:
+                rows = np.frombuffer(arr, np.int64).reshape(len(arr), -1)
+                if (rows[rows[:, numel] > 0, :2] % 16).any():
+                    raise ValueError("parameters and gradients must be 16-byte aligned")
+            self.grad_norm = clip_grad_norm_([p for g in self.param_groups for p in g["params"]], self.max_grad_norm)
+        for group, arr in todo:
             group["step"] = group.get("step", 0) + 1
             self._run(group, arr)
         return loss

@@ -32,3 +32,50 @@ def test_a_repeated_parameter_counts_and_is_clipped_once(calls, limit):
     optim.clip_grad_norm_([a, b, a, a], limit)
     passed = calls[0][1][0]
     assert len(passed) == 2 and passed[0] is a.grad and passed[1] is b.grad
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says that it is on a GPU."""
+    is_cuda = True
+
+
+def refused_params():
+    """Two groups' parameters, the last one's gradient of a type that clipping takes and no step."""
+    ps = [torch.nn.Parameter(torch.zeros(n, dtype=BF).as_subclass(OnGpu)) for n in (5, 6, 5000)]
+    for p in ps:
+        p.grad = torch.ones(p.shape, dtype=BF)
+    return ps
+
+
+OPTIMIZERS = [optim.AdamW8bitSR, optim.Momentum8bitSR, optim.Lion8bitSR, optim.AdamWBF16SR]
+
+
+@pytest.fixture
+def prepared(monkeypatch):
+    monkeypatch.setattr(optim.B, "q8_prepare_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: torch.autograd.profiler.record_function("device"))
+
+
+@pytest.mark.parametrize("cls", OPTIMIZERS)
+@pytest.mark.parametrize("fault,limit", [("type", None), ("type", 0.5), ("layout", None), ("layout", 0.5), ("alignment", 0.5)])
+def test_a_refused_step_touches_nothing(calls, prepared, cls, limit, fault):
+    ps = refused_params()
+    empty = torch.nn.Parameter(torch.zeros(9, dtype=BF)[1:1].as_subclass(OnGpu))      # at no alignment, of no elements
+    empty.grad = torch.ones(9, dtype=BF)[1:1]
+    opt = cls([{"params": [*ps[:2], empty]}, {"params": ps[2:]}], max_grad_norm=limit)
+    opt.step()
+    assert len(calls) == (3 if limit else 2)
+    calls.clear()
+    before = opt.grad_norm
+    bad = {"type": lambda: torch.ones(5000), "layout": lambda: torch.ones(10000, dtype=BF)[::2],
+           "alignment": lambda: torch.ones(5008, dtype=BF)[1:5001]}[fault]()
+    if fault == "type":                              # torch itself refuses such a gradient but through .data
+        ps[2].data = torch.zeros(5000)
+        ps[2].grad = bad
+        ps[2].data = torch.zeros(5000, dtype=BF)
+    else:
+        ps[2].grad = bad
+    with pytest.raises(ValueError):
+        opt.step()
+    assert calls == [] and opt.grad_norm is before
+    assert [g["step"] for g in opt.param_groups] == [1, 1]
