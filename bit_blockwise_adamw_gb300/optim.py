@@ -48,10 +48,10 @@ def clip_grad_norm_(parameters, max_norm):
     synchronised yet.  Gradients are contiguous bf16 or float32 CUDA tensors of
     one device; a parameter that comes twice counts once.  max_norm infinite: the
     norm alone."""
-    params = [parameters] if torch.is_tensor(parameters) else parameters
-    grads = [p.grad for p in {id(p): p for p in params}.values() if p.grad is not None]
+    params = {id(p): p for p in ([parameters] if torch.is_tensor(parameters) else parameters)}.values()
+    grads = [p.grad for p in params if p.grad is not None]
     if not grads:
-        return torch.zeros(())
+        return torch.zeros((), device=next((p.device for p in params), None))
     norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
     if max_norm == float("inf"):
         B.q8_grad_norm(grads, norm)

@@ -79,3 +79,11 @@ def test_a_refused_step_touches_nothing(calls, prepared, cls, limit, fault):
         opt.step()
     assert calls == [] and opt.grad_norm is before
     assert [g["step"] for g in opt.param_groups] == [1, 1]
+
+
+def test_the_norm_of_no_gradients_is_on_the_parameters_device(calls):
+    p = torch.nn.Parameter(torch.zeros(5, dtype=BF, device="meta"))
+    for given in (p, [p], iter([p, p])):
+        norm = optim.clip_grad_norm_(given, 1.0)
+        assert norm.device.type == "meta" and norm.dim() == 0 and norm.dtype == torch.float32
+    assert float(optim.clip_grad_norm_([], 1.0)) == 0 and calls == []
