@@ -51,7 +51,7 @@ def clip_grad_norm_(parameters, max_norm):
     params = {id(p): p for p in ([parameters] if torch.is_tensor(parameters) else parameters)}.values()
     grads = [p.grad for p in params if p.grad is not None]
     if not grads:
-        return torch.zeros((), device=next((p.device for p in params), None))
+        return torch.zeros((), dtype=torch.float32, device=next((p.device for p in params), None))
     norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
     if max_norm == float("inf"):
         B.q8_grad_norm(grads, norm)

@@ -87,3 +87,11 @@ def test_the_norm_of_no_gradients_is_on_the_parameters_device(calls):
         norm = optim.clip_grad_norm_(given, 1.0)
         assert norm.device.type == "meta" and norm.dim() == 0 and norm.dtype == torch.float32
     assert float(optim.clip_grad_norm_([], 1.0)) == 0 and calls == []
+
+
+def test_the_norm_of_no_gradients_is_float32(calls):
+    torch.set_default_dtype(torch.float64)
+    try:
+        assert optim.clip_grad_norm_([torch.nn.Parameter(torch.zeros(3))], 1.0).dtype == torch.float32
+    finally:
+        torch.set_default_dtype(torch.float32)
