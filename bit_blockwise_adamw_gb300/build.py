@@ -4,7 +4,9 @@ Every translation unit is compiled by nvcc for sm_103a only, in parallel,
 then linked into one shared library that exports the C ABI of
 include/q8adamw.h.  Floating-point contraction is off (--fmad=false): each
 fp32 operation of the step rounds on its own.  Beside it goes a small CPython
-module of the binding (csrc/q8_lists.cpp, g++), for the installed torch.
+module of the binding (csrc/q8_lists.cpp, g++ and torch's headers), for the
+installed torch; where that does not compile, the library is built all the same,
+and the binding's calls on lists of gradients say that the module is missing.
 """
 import concurrent.futures as cf
 import glob
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -33,6 +36,13 @@ def lists_module():
 
 
 def _build_lists(force):
+    try:
+        _compile_lists(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn("q8_lists is not built, and q8_grad_norm and q8_clip_grads cannot be called from Python: %s" % e, RuntimeWarning)
+
+
+def _compile_lists(force):
     import torch
     src, out = os.path.join(CSRC, "q8_lists.cpp"), lists_module()
     inputs = [src, os.path.join(INCLUDE, "q8train.h"), os.path.abspath(__file__)]
@@ -45,10 +55,15 @@ def _build_lists(force):
            "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], src, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
-    os.replace(tmp, out)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
+        os.replace(tmp, out)
+    except (OSError, RuntimeError):
+        if os.path.exists(out):
+            os.remove(out)                               # of older sources
+        raise
 
 
 def nvcc():
@@ -93,7 +108,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 4)) as ex:
         lists = ex.submit(_build_lists, force)
         results = list(ex.map(compile_one, _sources()))
-        lists.result()
     if verbose:
         for _, log in results:
             if log.strip():
@@ -105,6 +119,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    lists.result()
     return LIB
 
 
