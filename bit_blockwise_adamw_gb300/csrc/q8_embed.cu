@@ -694,8 +694,8 @@ struct Columns {
     static __device__ __forceinline__ bool off4(const T* row) { return reinterpret_cast<uintptr_t>(row) % 4 != 0; }
 
     // slot: this thread's, kRowThreads vectors apart.  edge: the row is the first
-    // or the last of its matrix, and the words that its pairs lie in may reach
-    // past it.
+    // or one of the last two of its matrix, and the words that its pairs lie in
+    // may reach past it.
     __device__ __forceinline__ void fetch(uint4* slot, const T* row, bool edge) const
     {
         if constexpr (VEC) {
@@ -895,7 +895,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) sum_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < kStep; ++j) {
             const uint32_t t = __shfl_sync(~0u, tokens, (i + j) & 31);
-            if (on && i + j < count) cols.fetch(slot + j * (kVecs * kRowThreads), dout + static_cast<int64_t>(t) * a.stride, t == 0 || t == N - 1);
+            // a row's words reach up to two elements past it, which are the next two rows where rows are single elements
+            if (on && i + j < count) cols.fetch(slot + j * (kVecs * kRowThreads), dout + static_cast<int64_t>(t) * a.stride, t == 0 || t + 2 >= N);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
