@@ -811,20 +811,18 @@ __device__ __forceinline__ uint64_t entry_at(const uint64_t* sorted, int64_t i, 
     return i >= 0 && i < n ? __ldcg(reinterpret_cast<const unsigned long long*>(sorted) + i) : none;
 }
 
-// Zeros of one CTA's rows [begin, end), those that no token has.
+// Zeros of one CTA's rows [begin, end), a thread for each at most: those that no
+// token has.
 __device__ void fill_absent(const SumArgs& a, int64_t begin, int64_t end)
 {
-    __shared__ uint32_t present[kRowThreads / 32];
+    constexpr int kWarps = kRowThreads / 32;
+    __shared__ uint32_t present[kWarps];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    for (int64_t first = begin; first < end; first += kRowThreads) {
-        const uint32_t some = __ballot_sync(~0u, first + threadIdx.x < end && a.r.present[first + threadIdx.x]);
-        __syncthreads();
-        if (lane == 0) present[warp] = some;
-        __syncthreads();
-        const int rows = static_cast<int>(min(int64_t(kRowThreads), end - first));
-        constexpr int kWarps = kRowThreads / 32;
-        zero_absent(a.dtable, a.e.dim, first, rows * warp / kWarps, rows * (warp + 1) / kWarps, present, lane);
-    }
+    const uint32_t some = __ballot_sync(~0u, begin + threadIdx.x < end && a.r.present[begin + threadIdx.x]);
+    if (lane == 0) present[warp] = some;
+    __syncthreads();
+    const int rows = static_cast<int>(end - begin);
+    zero_absent(a.dtable, a.e.dim, begin, rows * warp / kWarps, rows * (warp + 1) / kWarps, present, lane);
 }
 
 template <typename T, bool VEC>
