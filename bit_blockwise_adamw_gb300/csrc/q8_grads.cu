@@ -8,10 +8,13 @@
 // tensor is cut into chunks of 32 KB that start on 16 bytes (the few
 // elements before the first and behind the last whole vector of eight go one by
 // one).  The CTAs take the chunks in turn, and each leaves one sum of squares in
-// the workspace, in double; whoever needs the norm adds these up in one fixed
-// order, without double arithmetic.  Clipping reads the gradients a second time,
-// from the end backwards, so that what was read last, and is still in L2, comes
-// first, a CTA for each chunk.
+// the workspace, in double; whoever needs the norm adds these up, without double
+// arithmetic.  Clipping reads the gradients a second time, a CTA for each chunk,
+// each launch's from the end backwards, so that what was read last, and is still
+// in L2, comes first.  (Of several launches the first comes first: lists beyond
+// 768 tensors find only the last launch's end in L2, if that.)  Every CTA of the
+// clipping adds up all launches' sums: 7680 tensors of 20000 bf16 take 471 us, as
+// one tensor 134; 76800 of them 12.6 ms, as one 1.33.
 //
 // Measured: the norm of 6.66e9 bf16 1.80 ms (7.4 TB/s of reads); clipping of
 // 1.56e9 bf16 1.35 ms (9.35 GB moved, 6.9 TB/s; with as many CTAs as run at
@@ -66,7 +69,7 @@ struct GradArgs {
     int64_t nchunks;
     float max_norm;
     int32_t each;              // chunks of a CTA of clip_kernel
-    int32_t keep;              // last chunks, which L2 is to keep for the second pass
+    int32_t keep;              // the launch's last chunks, which L2 is to keep for the second pass
     int32_t nt;
     int32_t parts_at;          // this launch's place in parts
     int32_t nparts;            // all launches' sums
@@ -122,8 +125,10 @@ __device__ __forceinline__ void add_squares(const Eight<T>& v, float2 (&sum)[2])
 // The squares of a thread's vectors p, p + kGradThreads * 8, ... before `stop`
 // again, where their sum shows that some may have left fp32's range: the largest
 // magnitude picks a power of two that brings all of them, or all that count,
-// back into it.  Out of line, and read again, so that the loop that hardly ever
-// comes here keeps its registers.
+// back into it.  Out of line, and read again, so that the loop keeps its registers.
+// Zeros and values below some 4e-12 come here, too, and take longer: the norm of
+// 50257 x 4096 bf16 62 us, 94 with nine rows of ten zeros, 108 of zeros alone, 194
+// of values near 1e-13 (float32 121, 194, 217 and 387).
 template <typename T>
 __device__ __noinline__ double squares_scaled(const T* p, const T* stop)
 {
